@@ -11,6 +11,8 @@ Entry points (same names as include/adaspark.h, without the prefix):
 ``attn_read_stats``, ``token_ffn``, ``token_ffn_backward``, ``ffn_export_active``,
 ``ffn_read_stats``,
 ``layer``, ``layer_buffers``, ``rmsnorm``,
+``rope_frequencies``, ``qk_rope``, ``qk_rope_append``, ``qk_rope_backward``, ``kv_append``,
+``kv_plan``, ``decode_attn``,
 ``read_device_status``, ``timer_enable``, ``timer_read``, ``launch_count``,
 ``device_check``, ``status_string``.
 """
@@ -25,9 +27,11 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libadaspar
 
 OK, EINVAL, ECUDA, EUNSUPPORTED, EDEVICE = 0, -1, -2, -3, -4
 BF16, FP32 = 0, 1
-DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_RANGE = 0x1, 0x2, 0x4
+DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_RANGE, DEV_PAGES = 0x1, 0x2, 0x4, 0x8
 # AdaS-FFN token importance (ADASPARK_IMPORTANCE_*)
 IMPORTANCE_L2_SHARE, IMPORTANCE_L2SQ_SHARE, IMPORTANCE_SOFTMAX = 0, 1, 2
+# scaling of rotary frequencies (ADASPARK_ROPE_*)
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 
 
 class AdasparkError(RuntimeError):
@@ -70,6 +74,10 @@ def lib():
         L = ctypes.CDLL(_LIB_PATH)
         vp, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
         i32p = ctypes.POINTER(ctypes.c_int32)
+        i64, f64 = ctypes.c_int64, ctypes.c_double
+        # positions, axes, sections, freq, rot, interleaved, magnitude, w_q, w_k, eps
+        rope = [vp, i32, i32p, vp, i32, i32, f32, vp, vp, f32]
+        cache = [vp, vp, i64, i64, i64, i32, i32]   # k, v, strides, pages, page size
         sigs = {
             "adaspark_status_string": (ctypes.c_char_p, [i32]),
             "adaspark_cube_count": (i32, [i32] * 6 + [i32p]),
@@ -102,6 +110,22 @@ def lib():
             "adaspark_layer": (i32, [vp] * 8 + [i32, vp, vp, vp] + [i32] * 8 +
                                [f32, f32, vp, vp, sz, vp]),
             "adaspark_rmsnorm": (i32, [vp, i32, vp, vp, i32, i32, f32, vp]),
+            "adaspark_rope_frequencies": (i32, [i32, f64, i32, f64, i32, ctypes.POINTER(f64),
+                                                ctypes.POINTER(f32)]),
+            "adaspark_qk_rope": (i32, [vp, i64, i64] * 2 + [i32] + rope + [i32] * 4 +
+                                 [vp, i64, i64] * 2 + [vp]),
+            "adaspark_qk_rope_append": (i32, [vp, i64, i64] * 3 + [i32] + rope + [i32] * 4 +
+                                        [vp] + cache + [vp, i64, i64, vp]),
+            "adaspark_kv_append": (i32, [vp, i64, i64] * 2 + [i32] * 4 + [vp] + cache + [vp]),
+            "adaspark_qk_rope_backward_workspace": (sz, [i32] * 5),
+            "adaspark_qk_rope_backward": (i32, ([vp, i64, i64] * 2 + [i32]) * 2 + rope +
+                                          [i32] * 4 + [vp] * 5 + [sz, vp]),
+            "adaspark_kv_plan_workspace": (sz, [i32]),
+            "adaspark_kv_plan": (i32, [vp, vp, i32, i32, vp, i64, i32, vp, i32] + [vp] * 4 +
+                                 [i32, vp, sz, vp]),
+            "adaspark_decode_attn_workspace": (sz, [i32] * 5),
+            "adaspark_decode_attn": (i32, [vp, i64, i64] + cache + [i32, vp, i64, i32, vp] +
+                                     [i32] * 4 + [f32, vp, vp, vp, sz, vp]),
             "adaspark_ffn_export_active": (i32, [vp] + [i32] * 6 + [vp, vp]),
             "adaspark_ffn_read_stats": (i32, [vp, ctypes.POINTER(_FfnStats), vp]),
             "adaspark_read_device_status": (i32, [vp, ctypes.POINTER(ctypes.c_uint32), vp]),
@@ -491,6 +515,345 @@ def rmsnorm(x, weight=None, eps=1e-6, out=None, stream=None):
                                   else None, _ptr(out), n, D, float(eps), _stream(stream)),
            "adaspark_rmsnorm")
     return out
+
+
+# ----------------------------------------------------------------- generation
+def _stream_of(device, stream):
+    """The raw stream of a call on `device`; a call on another stream or device
+    than the current ones runs (and allocates) inside _Elsewhere."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream
+
+
+class _Elsewhere:
+    """Makes `stream` and its device the current ones for a call, so that what
+    the call allocates belongs to the stream that uses it."""
+
+    def __init__(self, stream):
+        import torch
+        self.ctx = None
+        if (stream.device.index != torch.cuda.current_device()
+                or stream != torch.cuda.current_stream()):
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _rows(t, name, dtype, device, shape=None):
+    """(pointer, token stride, head stride) of a [tokens, heads, d] tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != shape):
+        want = shape if shape is not None else "[tokens, heads, d]"
+        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), ts, hs
+
+
+def _flat(t, name, dtype, device, shape):
+    """Pointer of a dense tensor of the given shape."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _bytes(t, device):
+    """(pointer, bytes) of a workspace."""
+    import torch
+    if not t.is_cuda or t.device != device or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return t.data_ptr(), t.numel()
+
+
+def _rope_args(n, d, dtype, device, positions, freq, w_q, w_k, eps, interleaved, sections,
+               magnitude):
+    import torch
+    rot = 0
+    axes, sec, pos, fr = 1, None, None, None
+    if freq is not None:
+        rot = 2 * freq.numel()
+        fr = _flat(freq, "freq", torch.float64, device, (rot // 2,))
+        if positions is None:
+            raise ValueError("positions is required")
+        if sections is not None:
+            axes = 3
+            if len(sections) != 3:
+                raise ValueError("sections must be three numbers of pairs")
+            sec = (ctypes.c_int32 * 3)(*(int(x) for x in sections))
+        pos = _flat(positions, "positions", torch.int32, device, (3, n) if axes == 3 else (n,))
+    wq = None if w_q is None else _flat(w_q, "w_q", dtype, device, (d,))
+    wk = None if w_k is None else _flat(w_k, "w_k", dtype, device, (d,))
+    return pos, axes, sec, fr, rot, 1 if interleaved else 0, magnitude, wq, wk, eps
+
+
+def _cache_args(k_cache, v_cache, hkv, d, dtype, device):
+    """k, v, strides, pages and page size of a [pages, page_size, hkv, d] cache."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 4 or t.shape[2] != hkv or t.shape[3] != d:
+            raise ValueError(f"{name} must be [pages, page_size, {hkv}, {d}], got "
+                             f"{tuple(t.shape)}")
+        if t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name} must be {dtype} on {device}, got {t.dtype} on {t.device}")
+    ps, ts, hs, es = k_cache.stride()
+    if es != 1 or v_cache.stride() != (ps, ts, hs, es) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape and strides, with the "
+                         "elements of a head contiguous")
+    return k_cache.data_ptr(), v_cache.data_ptr(), ps, ts, hs, k_cache.shape[0], k_cache.shape[1]
+
+
+def rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_len=0):
+    """Host call: (freq float64 [rot/2], magnitude) of rotary positions, scaled
+    for long contexts by ``scaling`` (ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN)."""
+    freq = np.empty(max(int(rot), 0) // 2, np.float64)
+    mag = ctypes.c_float(0.0)
+    _check(lib().adaspark_rope_frequencies(
+        int(rot), float(base), int(scaling), float(factor), int(original_len),
+        freq.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), ctypes.byref(mag)),
+        "adaspark_rope_frequencies")
+    return freq, mag.value
+
+
+def qk_rope(Q, K, positions, freq, w_q=None, w_k=None, eps=1e-6, interleaved=False, sections=None,
+            magnitude=1.0, out_q=None, out_k=None, stream=None):
+    """Per-head RMSNorm (with ``w_q`` / ``w_k``) and rotary positions of Q
+    [N, hq, d] and K [N, hkv, d] (any token and head strides): returns the
+    rotated (Q, K). ``freq`` float64 [rot/2] on the device, ``positions`` int32
+    [N], or [3, N] with ``sections`` (pairs per axis). ``out_q`` / ``out_k`` may be
+    Q / K themselves."""
+    import torch
+    dev, dt = Q.device, Q.dtype
+    code = _dtype_code(Q)
+    q = _rows(Q, "Q", dt, dev)
+    n, hq, d = Q.shape
+    k = _rows(K, "K", dt, dev, (n, K.shape[1], d))
+    hkv = K.shape[1]
+    args = _rope_args(n, d, dt, dev, positions, freq, w_q, w_k, eps, interleaved, sections,
+                      magnitude)
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        if out_q is None:
+            out_q = torch.empty((n, hq, d), dtype=dt, device=dev)
+        if out_k is None:
+            out_k = torch.empty((n, hkv, d), dtype=dt, device=dev)
+        qo = _rows(out_q, "out_q", dt, dev, (n, hq, d))
+        ko = _rows(out_k, "out_k", dt, dev, (n, hkv, d))
+        _check(lib().adaspark_qk_rope(*q, *k, code, *args, n, hq, hkv, d, *qo, *ko,
+                                      s.cuda_stream), "adaspark_qk_rope")
+    return out_q, out_k
+
+
+def qk_rope_append(Q, K, V, positions, freq, slots, k_cache, v_cache, w_q=None, w_k=None, eps=1e-6,
+                   interleaved=False, sections=None, magnitude=1.0, out_q=None, stream=None):
+    """qk_rope of a step's tokens with the rotated keys, and V, written into the
+    paged cache [pages, page_size, hkv, d] at ``slots`` int32 [N] (-1: not
+    cached); returns the rotated Q."""
+    import torch
+    dev, dt = Q.device, Q.dtype
+    code = _dtype_code(Q)
+    q = _rows(Q, "Q", dt, dev)
+    n, hq, d = Q.shape
+    hkv = K.shape[1]
+    k = _rows(K, "K", dt, dev, (n, hkv, d))
+    v = _rows(V, "V", dt, dev, (n, hkv, d))
+    sl = _flat(slots, "slots", torch.int32, dev, (n,))
+    cache = _cache_args(k_cache, v_cache, hkv, d, dt, dev)
+    args = _rope_args(n, d, dt, dev, positions, freq, w_q, w_k, eps, interleaved, sections,
+                      magnitude)
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        if out_q is None:
+            out_q = torch.empty((n, hq, d), dtype=dt, device=dev)
+        qo = _rows(out_q, "out_q", dt, dev, (n, hq, d))
+        _check(lib().adaspark_qk_rope_append(*q, *k, *v, code, *args, n, hq, hkv, d, sl, *cache,
+                                             *qo, s.cuda_stream), "adaspark_qk_rope_append")
+    return out_q
+
+
+def kv_append(K, V, slots, k_cache, v_cache, stream=None):
+    """K and V [N, hkv, d] as they are into the paged cache at ``slots`` (-1: not
+    cached)."""
+    import torch
+    dev, dt = K.device, K.dtype
+    code = _dtype_code(K)
+    k = _rows(K, "K", dt, dev)
+    n, hkv, d = K.shape
+    v = _rows(V, "V", dt, dev, (n, hkv, d))
+    sl = _flat(slots, "slots", torch.int32, dev, (n,))
+    cache = _cache_args(k_cache, v_cache, hkv, d, dt, dev)
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        _check(lib().adaspark_kv_append(*k, *v, code, n, hkv, d, sl, *cache, s.cuda_stream),
+               "adaspark_kv_append")
+
+
+def qk_rope_backward_workspace_bytes(n_tokens, hq, hkv, d, dtype=BF16) -> int:
+    return int(lib().adaspark_qk_rope_backward_workspace(n_tokens, hq, hkv, d, dtype))
+
+
+def qk_rope_backward(dQ_out, dK_out, positions, freq, Q=None, K=None, w_q=None, w_k=None, eps=1e-6,
+                     interleaved=False, sections=None, magnitude=1.0, dQ=None, dK=None, dw_q=None,
+                     dw_k=None, workspace=None, stream=None):
+    """Backward of qk_rope: upstream gradients (bf16 or fp32) of its outputs;
+    Q and K are its inputs, needed where a weight is given. Returns (dQ, dK,
+    dw_q, dw_k, workspace), fp32; dw_q / dw_k are None without their weight."""
+    import torch
+    dev = dQ_out.device
+    dy = dQ_out.dtype
+    f32 = torch.float32
+    gq = _rows(dQ_out, "dQ_out", dy, dev)
+    n, hq, d = dQ_out.shape
+    hkv = dK_out.shape[1]
+    gk = _rows(dK_out, "dK_out", dy, dev, (n, hkv, d))
+    dt = w_q.dtype if w_q is not None else w_k.dtype if w_k is not None else dy
+    code = _dtype_code(w_q if w_q is not None else w_k if w_k is not None else dQ_out)
+    q = k = (None, 0, 0)
+    if w_q is not None:
+        if Q is None:
+            raise ValueError("Q is required with w_q")
+        q = _rows(Q, "Q", dt, dev, (n, hq, d))
+    if w_k is not None:
+        if K is None:
+            raise ValueError("K is required with w_k")
+        k = _rows(K, "K", dt, dev, (n, hkv, d))
+    args = _rope_args(n, d, dt, dev, positions, freq, w_q, w_k, eps, interleaved, sections,
+                      magnitude)
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        dQ = torch.empty((n, hq, d), dtype=f32, device=dev) if dQ is None else dQ
+        dK = torch.empty((n, hkv, d), dtype=f32, device=dev) if dK is None else dK
+        ptrs = [_flat(dQ, "dQ", f32, dev, (n, hq, d)), _flat(dK, "dK", f32, dev, (n, hkv, d))]
+        if w_q is None:
+            dw_q = None
+        elif dw_q is None:
+            dw_q = torch.empty(d, dtype=f32, device=dev)
+        if w_k is None:
+            dw_k = None
+        elif dw_k is None:
+            dw_k = torch.empty(d, dtype=f32, device=dev)
+        ptrs += [None if t is None else _flat(t, nm, f32, dev, (d,))
+                 for t, nm in ((dw_q, "dw_q"), (dw_k, "dw_k"))]
+        if workspace is None and (w_q is not None or w_k is not None):
+            nb = qk_rope_backward_workspace_bytes(n, hq, hkv, d, code)
+            if nb == 0:
+                raise AdasparkError(EINVAL, "adaspark_qk_rope_backward_workspace")
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        ws = (None, 0) if workspace is None else _bytes(workspace, dev)
+        _check(lib().adaspark_qk_rope_backward(*gq, *gk, _dtype_code(dQ_out), *q, *k, code, *args,
+                                               n, hq, hkv, d, *ptrs, *ws, s.cuda_stream),
+               "adaspark_qk_rope_backward")
+    return dQ, dK, dw_q, dw_k, workspace
+
+
+def kv_plan_workspace_bytes(n_seqs) -> int:
+    return int(lib().adaspark_kv_plan_workspace(n_seqs))
+
+
+def kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_rows, slots=None,
+            positions=None, token_starts=None, workspace=None, stream=None):
+    """One step's page plan on the device (adaspark_kv_plan): updates
+    ``block_table`` int32 [n_seqs, max_pages], ``free_pages`` int32 [n_pages] and
+    ``n_free`` int32 [1] in place; returns (slots [n_rows], positions [n_rows],
+    token_starts [n_seqs + 1], workspace). read_device_status(workspace) tells
+    whether the plan was carried out."""
+    import torch
+    dev, i32 = old_lens.device, torch.int32
+    ns = old_lens.numel()
+    old, new = (_flat(t, nm, i32, dev, (ns,)) for t, nm in ((old_lens, "old_lens"),
+                                                            (new_lens, "new_lens")))
+    if (not block_table.is_cuda or block_table.dtype != i32 or block_table.device != dev
+            or block_table.dim() != 2 or block_table.shape[0] != ns
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+        raise ValueError(f"block_table must be int32 [{ns}, max_pages] on {dev}, rows contiguous")
+    n_pages = free_pages.numel()
+    fp = _flat(free_pages, "free_pages", i32, dev, (n_pages,))
+    nf = _flat(n_free, "n_free", i32, dev, (1,))
+    n_rows = int(n_rows)
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        if slots is None:
+            slots = torch.empty(n_rows, dtype=i32, device=dev)
+        if positions is None:
+            positions = torch.empty(n_rows, dtype=i32, device=dev)
+        if token_starts is None:
+            token_starts = torch.empty(ns + 1, dtype=i32, device=dev)
+        outs = (_flat(token_starts, "token_starts", i32, dev, (ns + 1,)),
+                _flat(slots, "slots", i32, dev, (n_rows,)),
+                _flat(positions, "positions", i32, dev, (n_rows,)))
+        if workspace is None:
+            nb = kv_plan_workspace_bytes(ns)
+            if nb == 0:
+                raise AdasparkError(EINVAL, "adaspark_kv_plan_workspace")
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _check(lib().adaspark_kv_plan(old, new, ns, int(page_size), block_table.data_ptr(),
+                                      block_table.stride(0), block_table.shape[1], fp, n_pages, nf,
+                                      *outs, n_rows, *_bytes(workspace, dev), s.cuda_stream),
+               "adaspark_kv_plan")
+    return slots, positions, token_starts, workspace
+
+
+def decode_attn_workspace_bytes(n_seqs, hq, hkv, d, dtype=BF16) -> int:
+    return int(lib().adaspark_decode_attn_workspace(n_seqs, hq, hkv, d, dtype))
+
+
+def decode_attn(Q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None, lse=None,
+                workspace=None, stream=None):
+    """Attention of one new token per sequence, Q [n_seqs, hq, d], over the paged
+    cache [pages, page_size, hkv, d] (any outer strides): ``block_table`` int32
+    [n_seqs, max_pages], ``seq_lens`` int32 [n_seqs]; ``scale`` defaults to
+    1/sqrt(d). Returns (out, lse fp32 [n_seqs, hq], workspace)."""
+    import torch
+    dev, dt, i32 = Q.device, Q.dtype, torch.int32
+    code = _dtype_code(Q)
+    q = _rows(Q, "Q", dt, dev)
+    n, hq, d = Q.shape
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, hkv, d]")
+    hkv = k_cache.shape[2]
+    cache = _cache_args(k_cache, v_cache, hkv, d, dt, dev)
+    if (not block_table.is_cuda or block_table.dtype != i32 or block_table.device != dev
+            or block_table.dim() != 2 or block_table.shape[0] != n
+            or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+        raise ValueError(f"block_table must be int32 [{n}, max_pages] on {dev}, rows contiguous")
+    lens = _flat(seq_lens, "seq_lens", i32, dev, (n,))
+    s = _stream_of(dev, stream)
+    with _Elsewhere(s):
+        if out is None:
+            out = torch.empty((n, hq, d), dtype=dt, device=dev)
+        if lse is None:
+            lse = torch.empty((n, hq), dtype=torch.float32, device=dev)
+        o = _flat(out, "out", dt, dev, (n, hq, d))
+        ls = _flat(lse, "lse", torch.float32, dev, (n, hq))
+        if workspace is None:
+            nb = decode_attn_workspace_bytes(n, hq, hkv, d, code)
+            if nb == 0:
+                raise AdasparkError(EINVAL, "adaspark_decode_attn_workspace")
+            workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _check(lib().adaspark_decode_attn(*q, *cache, code, block_table.data_ptr(),
+                                          block_table.stride(0), block_table.shape[1], lens, n, hq,
+                                          hkv, d, d ** -0.5 if scale is None else float(scale), o,
+                                          ls, *_bytes(workspace, dev), s.cuda_stream),
+               "adaspark_decode_attn")
+    return out, lse, workspace
 
 
 def ffn_export_active(workspace, n_tokens, n_vis, n_cubes, D, F, dtype, stream=None):

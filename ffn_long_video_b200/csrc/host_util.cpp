@@ -96,6 +96,25 @@ int device_is_sm100() {
   return (major == 10 && minor == 0) ? 1 : 0;
 }
 
+int current_device(int* sms) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices] = {};  // SM count of an sm_100 device, -1 of another
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ADASPARK_ECUDA;
+  if (dev < 0 || dev >= kMaxDevices) return ADASPARK_EUNSUPPORTED;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const int ok = device_is_sm100();
+    if (ok < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return ADASPARK_ECUDA;
+    if (!ok) n = -1;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  if (n < 0) return ADASPARK_EUNSUPPORTED;
+  if (sms) *sms = n;
+  return ADASPARK_OK;
+}
+
 }  // namespace adaspark
 
 using namespace adaspark;

@@ -50,4 +50,8 @@ inline bool aligned(const void* ptr, size_t a) {
 
 int device_is_sm100();  // 1 yes, 0 no, -1 query failed
 
+// ADASPARK_OK when the current device is an sm_100 GPU; *sms (if not NULL) gets
+// its SM count. Looked up once per device.
+int current_device(int* sms);
+
 }  // namespace adaspark

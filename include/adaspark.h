@@ -63,6 +63,8 @@ typedef enum { ADASPARK_BF16 = 0, ADASPARK_FP32 = 1 } adaspark_dtype;
                                         /* row then keeps only its own cube); AdaS-FFN: a  */
                                         /* SwiGLU activation or a W_down weight beyond the */
                                         /* fp16 range +-65504 (see adaspark_token_ffn)     */
+#define ADASPARK_DEV_PAGES        0x8u  /* adaspark_kv_plan: the free list holds too few    */
+                                        /* pages for the new lengths                        */
 
 /* Human-readable name of a return code. Never NULL. */
 const char *adaspark_status_string(int status);
@@ -462,6 +464,183 @@ int adaspark_layer_buffers(int n_tokens, int n_vis, int n_cubes, int hq, int hkv
  * unknown dtype. */
 int adaspark_rmsnorm(const void *x, int x_dtype, const void *weight, void *out, int n_rows, int D,
                      float eps, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Generation: rotary positions, the paged key-value cache, one new token.   */
+/* (The AdaSpark pages describe the prompt's sparse layer; a text token      */
+/* attends densely to every earlier token, and these calls carry that on     */
+/* from the prompt's keys and values, token by token.)                       */
+/* ------------------------------------------------------------------------ */
+
+/* Conventions of these calls, besides the shared ones above:
+ *   - Rows of heads have strides, in elements: element (t, h, e) of Q lies at
+ *     t * q_ts + h * q_hs + e, so the parts of one fused projection, or heads
+ *     outside tokens, are passed as they are. Bases are 16-byte aligned and
+ *     strides whole multiples of 16 bytes (else ADASPARK_EINVAL). Rows that
+ *     are written must not share memory.
+ *   - Paged cache: keys and values in two arrays of the same strides, element
+ *     (page, offset, head, e) at page * c_ps + offset * c_ts + head * c_hs + e;
+ *     pages lie one after another (c_ps >= a page's extent), tokens and heads
+ *     of a page in either order. A token's slot is page * page_size + offset;
+ *     n_pages * page_size < 2^31. Element offsets are 64-bit.
+ *   - Element type `dtype` (BF16 or FP32) is that of activations, norm weights
+ *     and cache; d = 64 or 128; hq % hkv == 0, hq <= 4096.
+ *   - ADASPARK_EUNSUPPORTED on a device that is not sm_100. */
+
+/* Scaling of rotary frequencies for contexts longer than the trained ones. */
+#define ADASPARK_ROPE_PLAIN  0  /* freq_i = base^(-2i/rot)                               */
+#define ADASPARK_ROPE_LINEAR 1  /* freq_i / factor (position interpolation)              */
+#define ADASPARK_ROPE_NTK    2  /* base * factor^(rot / (rot - 2)) in place of base      */
+#define ADASPARK_ROPE_YARN   3  /* by r = original_len * freq_i / 2 pi, the turns a pair */
+                                /* makes over the original length: freq_i from 32 turns, */
+                                /* freq_i / factor up to 1, linear in r between; the     */
+                                /* magnitude is 0.1 ln(factor) + 1                       */
+
+/* Rotary frequencies of rot/2 pairs (host only): freq [rot/2] in radians per
+ * position and the magnitude for adaspark_qk_rope. `factor` (>= 1) is unused by
+ * PLAIN, original_len (>= 1) used by YARN alone. ADASPARK_EINVAL for NULL
+ * pointers, rot odd or < 2 (NTK: < 4), base <= 1, or a factor that is not
+ * finite or < 1. */
+int adaspark_rope_frequencies(int rot, double base, int scaling, double factor, int original_len,
+                              double *freq, float *magnitude);
+
+/* Per-head RMSNorm (optional) and rotary positions of queries and keys, one
+ * pass. For each head x of Q (weight w = w_q) and of K (w = w_k):
+ *   n = x / sqrt(mean(x^2) + eps) * w   (n = x when w is NULL);
+ *   pair i < rot/2, elements (f, s) = (i, i + rot/2), or (2i, 2i + 1) when
+ *   `interleaved`, at the angle a = position * freq[i]:
+ *     out_f = magnitude * (n_f cos a - n_s sin a)
+ *     out_s = magnitude * (n_s cos a + n_f sin a)
+ *   out_e = n_e for e >= rot.
+ *
+ *   positions: device int32 [n_tokens] (n_axes = 1), or [3, n_tokens]
+ *       (n_axes = 3: time, height, width of a video token; sections[3], host,
+ *       sums to rot/2: the first sections[0] pairs follow axis 0, the next
+ *       sections[1] axis 1, the rest axis 2). Any int32 value.
+ *   freq: device float64 [rot/2]; rot a multiple of 16, 0 <= rot <= d (0: no
+ *       rotation, positions and freq may be NULL). Angles are reduced in 64
+ *       bits; norms and rotation in fp32, one rounding to `dtype` at the end.
+ *   w_q, w_k [d]: device, or NULL.
+ *   Q_out, K_out: may be Q, K themselves with the same strides (in place).
+ * n_tokens = 0 does nothing (arrays may then be NULL). Errors: ADASPARK_EINVAL for NULL pointers, bad
+ * sizes, strides or alignment, eps < 0 or NaN, a magnitude that is not finite. */
+int adaspark_qk_rope(const void *Q, int64_t q_ts, int64_t q_hs, const void *K, int64_t k_ts,
+                     int64_t k_hs, int dtype, const int32_t *positions, int n_axes,
+                     const int32_t *sections, const double *freq, int rot, int interleaved,
+                     float magnitude, const void *w_q, const void *w_k, float eps, int n_tokens,
+                     int hq, int hkv, int d, void *Q_out, int64_t qo_ts, int64_t qo_hs,
+                     void *K_out, int64_t ko_ts, int64_t ko_hs, void *stream);
+
+/* adaspark_qk_rope for the tokens of a step: the rotated keys, and V as it is,
+ * go into the cache at slots[t] (device int32 [n_tokens]) in the same pass;
+ * Q_out as above. A token whose slot is not in [0, n_pages * page_size) is not
+ * cached (-1 marks the rows that pad a batch); its Q_out is written all the
+ * same. Slots that occur twice leave either token's row, whole or mixed. */
+int adaspark_qk_rope_append(const void *Q, int64_t q_ts, int64_t q_hs, const void *K, int64_t k_ts,
+                            int64_t k_hs, const void *V, int64_t v_ts, int64_t v_hs, int dtype,
+                            const int32_t *positions, int n_axes, const int32_t *sections,
+                            const double *freq, int rot, int interleaved, float magnitude,
+                            const void *w_q, const void *w_k, float eps, int n_tokens, int hq,
+                            int hkv, int d, const int32_t *slots, void *k_cache, void *v_cache,
+                            int64_t c_ps, int64_t c_ts, int64_t c_hs, int n_pages, int page_size,
+                            void *Q_out, int64_t qo_ts, int64_t qo_hs, void *stream);
+
+/* Keys and values as they are into the cache (a prompt whose keys were rotated
+ * for adaspark_cube_attn): rows, slots and cache as for adaspark_qk_rope_append. */
+int adaspark_kv_append(const void *K, int64_t k_ts, int64_t k_hs, const void *V, int64_t v_ts,
+                       int64_t v_hs, int dtype, int n_tokens, int hkv, int d, const int32_t *slots,
+                       void *k_cache, void *v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,
+                       int n_pages, int page_size, void *stream);
+
+/* Device workspace bytes of adaspark_qk_rope_backward (0 for invalid sizes);
+ * it is used with a norm weight only. */
+size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d, int dtype);
+
+/* Backward of adaspark_qk_rope: with g the rotation's transpose applied to the
+ * upstream gradient (magnitude included), r = 1 / sqrt(mean(x^2) + eps):
+ *   no weight: dx = g;
+ *   weight:    dx = r (g w - x r mean(g w x r)),  dw = sum over tokens and heads of g x r.
+ *
+ *   dQ_out, dK_out: device, type dy_dtype (BF16 or FP32: adaspark_cube_attn_backward
+ *       writes FP32), strides as for Q and K;
+ *   Q, K: the forward's inputs (before the norm), needed where w_q / w_k is given;
+ *   dQ [n_tokens, hq, d], dK [n_tokens, hkv, d], dw_q, dw_k [d]: device float32,
+ *       written in full (not accumulated into); dw_q / dw_k needed and written
+ *       where the weight is given. dQ may be dQ_out itself, dK dK_out (FP32, dense).
+ *   workspace: as adaspark_qk_rope_backward_workspace says, 256-byte aligned;
+ *       may be NULL without weights.
+ * Sums in fp32 in a fixed order (no atomics). n_tokens = 0 sets dw_q, dw_k to
+ * zero. Errors as for adaspark_qk_rope. */
+int adaspark_qk_rope_backward(const void *dQ_out, int64_t dq_ts, int64_t dq_hs, const void *dK_out,
+                              int64_t dk_ts, int64_t dk_hs, int dy_dtype, const void *Q,
+                              int64_t q_ts, int64_t q_hs, const void *K, int64_t k_ts,
+                              int64_t k_hs, int dtype, const int32_t *positions, int n_axes,
+                              const int32_t *sections, const double *freq, int rot,
+                              int interleaved, float magnitude, const void *w_q, const void *w_k,
+                              float eps, int n_tokens, int hq, int hkv, int d, float *dQ,
+                              float *dK, float *dw_q, float *dw_k, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* Device workspace bytes of adaspark_kv_plan (0 when n_seqs < 1). */
+size_t adaspark_kv_plan_workspace(int n_seqs);
+
+/* One step's page plan, on the device: sequence i goes from old_lens[i] to
+ * new_lens[i] tokens. With P(n) = ceil(n / page_size) it keeps the first
+ * min(P(old), P(new)) entries of its block table row and takes
+ * P(new) - P(old) pages from the free list, or gives P(old) - P(new) back.
+ *   old_lens, new_lens [n_seqs]: device int32, 0 .. max_pages * page_size;
+ *   block_table: device int32, row i at i * table_stride, max_pages entries:
+ *       a sequence's pages in order; entries past P(new) keep what they held;
+ *   free_pages [n_pages], n_free [1]: device int32, the free pages
+ *       free_pages[0 .. n_free), updated in place; n_pages is the pool's size.
+ *       Pages are taken from its end, those given back in this plan first. A
+ *       plan from new to old lengths undoes the plan from old to new: tables,
+ *       list and count are as before.
+ *   token_starts [n_seqs + 1]: out, rows of earlier sequences' new tokens, then
+ *       the total;
+ *   slots, positions [n_rows]: out, slot and position of every new token
+ *       (sequences in order, positions ascending), -1 and 0 in rows past the
+ *       total (as adaspark_qk_rope_append takes them).
+ * A plan that cannot be carried out changes nothing but its outputs (starts 0,
+ * slots -1) and reports ADASPARK_DEV_PAGES (too few free pages) or
+ * ADASPARK_DEV_BAD_LAYOUT (a length out of range, more than n_rows new tokens,
+ * a free count or a gift the pool cannot hold); a page number outside
+ * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. The arrays
+ * must not overlap. workspace: 256-byte aligned. ADASPARK_EINVAL for NULL
+ * pointers, sizes < 1, a table_stride below max_pages, a short workspace. */
+int adaspark_kv_plan(const int32_t *old_lens, const int32_t *new_lens, int n_seqs, int page_size,
+                     int32_t *block_table, int64_t table_stride, int max_pages,
+                     int32_t *free_pages, int n_pages, int32_t *n_free, int32_t *token_starts,
+                     int32_t *slots, int32_t *positions, int n_rows, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Device workspace bytes of adaspark_decode_attn (0 for invalid sizes). */
+size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dtype);
+
+/* Attention of one new token per sequence over the paged cache (its own key
+ * and value appended before): for sequence i of n = seq_lens[i] keys, query
+ * head h and KV head floor(h / (hq/hkv)), z_j = scale * q . k_j:
+ *   lse = ln sum_{j<n} exp(z_j),  out = sum_{j<n} exp(z_j - lse) v_j;
+ *   n = 0, or every z_j = -inf: out = 0, lse = -inf.
+ *
+ *   Q: device, [n_seqs] rows of hq heads; block_table: device int32, row i at
+ *       i * table_stride, key j on page block_table[i][j / page_size];
+ *   seq_lens [n_seqs]: device int32, 0 .. max_pages * page_size;
+ *   scale: finite (1/sqrt(d) in adaspark_cube_attn);
+ *   out [n_seqs, hq, d]: device, dense; lse [n_seqs, hq]: device float32 or NULL;
+ *   workspace: 256-byte aligned.
+ * Nothing at or past a sequence's length is read (it may hold NaN). Values that
+ * are infinite or NaN among a sequence's keys make its results NaN or infinite.
+ * Results depend on the inputs, the sizes and max_pages alone (no atomics). A
+ * length out of range counts as 0 and a page number outside [0, n_pages) as
+ * absent keys; both report ADASPARK_DEV_BAD_LAYOUT. Errors: ADASPARK_EINVAL as
+ * for the other calls, or n_seqs or max_pages < 1. */
+int adaspark_decode_attn(const void *Q, int64_t q_ts, int64_t q_hs, const void *k_cache,
+                         const void *v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,
+                         int n_pages, int page_size, int dtype, const int32_t *block_table,
+                         int64_t table_stride, int max_pages, const int32_t *seq_lens, int n_seqs,
+                         int hq, int hkv, int d, float scale, void *out, float *lse,
+                         void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronize `stream` and read the status word of a workspace of either call.
  * Returns ADASPARK_OK, or ADASPARK_EDEVICE with *detail (if not NULL) holding the

@@ -28,6 +28,10 @@ Parity status per function (what pins it is in ``tests/test_oracle_pins.py``):
                             pinned (full central-difference Jacobians of the
                             pinned forward functions; torch autograd in float64
                             on the dense cases; sum invariants)
+* ``generation_ref`` (``rotate``, ``qk_rope``, ``qk_rope_backward``, ``kv_plan``,
+  ``decode_attn``)          pinned in ``tests/test_generation_cpu.py`` (complex
+                            products, central differences, replayed steps,
+                            softmax closed forms)
 * agreement with the authors' own numbers: parity unpinned (the pages print
   no worked example for any step; see the module docstring of adaspark_ref).
 """
@@ -56,3 +60,4 @@ from .adaspark_ref import (  # noqa: F401
     swiglu_ffn_backward,
     ffn_backward_given_sets,
 )
+from . import generation_ref  # noqa: F401

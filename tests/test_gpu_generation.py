@@ -1,0 +1,122 @@
+"""The calls as they are used together (needs a B200): a video prompt through
+rotary positions and AdaS-Attn, its keys and values into the paged cache, then
+text tokens one at a time - plan, rotate and append, attend.  A text token of
+AdaS-Attn attends densely to every earlier token, so each step's output is held
+to the prefill's row of the same token."""
+import numpy as np
+import pytest
+import torch
+
+import ffn_long_video_b200 as fb
+import workloads
+from oracle import generation_ref as gen
+from tests import parity
+
+pytestmark = pytest.mark.gpu
+
+CASES = {
+    "bf16": workloads.small_config(name="gen-bf16", grid=(4, 8, 8), cube=(4, 4, 4), n_text=24,
+                                   D=256, hq=8, hkv=2, F=256, seed=71),
+    "fp32-d64": workloads.small_config(name="gen-fp32", grid=(4, 8, 8), cube=(4, 4, 2), n_text=17,
+                                       D=256, hq=4, hkv=1, d=64, F=256, dtype="fp32", seed=72),
+}
+
+
+def video_positions(cfg):
+    """[3, N]: (t, h, w) of the video tokens in cube order, then text positions."""
+    T, H, W = cfg.grid
+    ch, cw, ct = cfg.cube
+    perm, _, _ = fb.cube_partition(T, H, W, ch, cw, ct, cfg.n_text)
+    t, rest = perm // (H * W), perm % (H * W)
+    vis = np.stack((t, rest // W, rest % W))
+    text = vis.max() + 1 + np.arange(cfg.n_text)
+    return np.concatenate((vis, np.broadcast_to(text, (3, cfg.n_text))), axis=1).astype(np.int32)
+
+
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("graph", [False, True])
+def test_decoding_continues_the_prompt(name, graph):
+    cfg = CASES[name]
+    case = parity.make_case(cfg)
+    t, N, n_new, page, d = case["t"], cfg.n_tokens, 9, 16, cfg.d
+    sections = (d // 8, 3 * d // 16, 3 * d // 16)
+    freq, mag = fb.rope_frequencies(d, 1e6)
+    freq = torch.from_numpy(freq).cuda()
+    pos = torch.from_numpy(video_positions(cfg)).cuda()
+    w = torch.ones(d, dtype=t["Q"].dtype, device="cuda")
+    kw = dict(w_q=w, w_k=w, sections=sections, magnitude=mag)
+    Qr, Kr = fb.qk_rope(t["Q"], t["K"], pos, freq, **kw)
+    want, ws = fb.cube_attn(Qr, Kr, t["V"], case["ids"], case["off"], cfg.n_vis, cfg.p)
+    assert fb.read_device_status(ws)[0] == fb.OK
+
+    # a batch of two sequences: the prompt twice, the second one shorter by three text tokens
+    lens = [N - n_new, N - n_new - 3]
+    cols = -(-N // page)
+    pool = 2 * cols + 3
+    table = torch.full((2, cols), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(pool, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    n_free = torch.tensor([pool], dtype=torch.int32, device="cuda")
+    k_cache = torch.full((pool, page, cfg.hkv, d), float("nan"), dtype=Kr.dtype, device="cuda")
+    v_cache = torch.full_like(k_cache, float("nan"))
+    cur = torch.zeros(2, dtype=torch.int32, device="cuda")
+    nxt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    slots, prompt_pos, starts, pws = fb.kv_plan(cur, nxt, table, free, n_free, page, sum(lens) + 5)
+    assert fb.read_device_status(pws)[0] == fb.OK
+    row = prompt_pos[:sum(lens)].long()
+    fb.kv_append(Kr[row], t["V"][row], slots[:sum(lens)].contiguous(), k_cache, v_cache)
+    cur.copy_(nxt)
+
+    # the step's buffers, as a captured loop keeps them; one padding row
+    rows = 3
+    q_in, k_in, v_in = (torch.zeros(rows, x.shape[1], d, dtype=x.dtype, device="cuda")
+                        for x in (t["Q"], t["K"], t["V"]))
+    pos3 = torch.zeros(3, rows, dtype=torch.int32, device="cuda")
+    b = {k: torch.empty(s, dtype=torch.int32, device="cuda")
+         for k, s in (("slots", rows), ("positions", rows), ("token_starts", 3))}
+    qr = torch.empty_like(q_in)
+    out = torch.empty(2, cfg.hq, d, dtype=Qr.dtype, device="cuda")
+    lse = torch.empty(2, cfg.hq, device="cuda")
+    dt = fb.BF16 if cfg.dtype == "bf16" else fb.FP32
+    dws = torch.empty(fb.decode_attn_workspace_bytes(2, cfg.hq, cfg.hkv, d, dt), dtype=torch.uint8,
+                      device="cuda")
+
+    def step():
+        fb.kv_plan(cur, nxt, table, free, n_free, page, rows, workspace=pws, **b)
+        fb.qk_rope_append(q_in, k_in, v_in, pos3, freq, b["slots"], k_cache, v_cache, out_q=qr, **kw)
+        fb.decode_attn(qr[:2], k_cache, v_cache, table, nxt, out=out, lse=lse, workspace=dws)
+        cur.copy_(nxt)
+
+    captured = None
+    outs = []
+    for i in range(n_new):
+        at = [lens[0] + i, lens[1] + i]
+        nxt.copy_(torch.tensor([x + 1 for x in at], dtype=torch.int32))
+        for buf, src in ((q_in, t["Q"]), (k_in, t["K"]), (v_in, t["V"])):
+            buf[:2] = src[at]
+        pos3[:, :2] = pos[:, at]
+        if graph and captured is None:
+            captured = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(captured):
+                step()
+        if graph:
+            captured.replay()
+        else:
+            step()
+        for x in (pws, dws):
+            assert fb.read_device_status(x)[0] == fb.OK
+        assert b["positions"].tolist() == at + [0] and b["slots"][2] == -1
+        # the rotated rows are the prefill's, so the cache holds the prompt's keys
+        assert torch.equal(qr[:2], Qr[at])
+        outs.append(out.clone())
+        if cfg.dtype == "bf16":
+            tol = dict(atol=2e-2, rtol=2.0 ** -7)     # two roundings of bf16, and the protocol's 2e-2
+        else:
+            tol = dict(atol=1e-4, rtol=1e-5)
+        assert torch.allclose(out.float(), want[at].float(), **tol), (i, (out - want[at]).abs().max())
+    # the last step against the float64 statement over the prefill's own keys
+    full = lambda x, n: x[:n].unsqueeze(0)  # noqa: E731
+    for s, n in enumerate((N, N - 3)):
+        o, l = gen.decode_attn(Qr[n - 1:n].cpu(), full(Kr, n).cpu().float().numpy(),
+                               full(t["V"], n).cpu().float().numpy(), np.zeros((1, 1), int), [n])
+        assert np.abs(lse[s].double().cpu().numpy() - l[0]).max() <= 1e-4
+        assert np.abs(out[s].double().cpu().numpy() - o[0]).max() <= (2e-2 if dt == fb.BF16 else 1e-4)
