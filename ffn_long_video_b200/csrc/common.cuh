@@ -151,6 +151,18 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
 }
 
 // ---------------------------------------------------------------------------
+// Kernels that follow one another closely (launch_after, host_util.h).
+// ---------------------------------------------------------------------------
+// Lets the stream's next kernel come up when every block has called this or ended.
+__device__ __forceinline__ void dependency_release() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Waits until the kernel before this one has ended and its writes are visible.
+__device__ __forceinline__ void dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // TMA (no multicast anywhere in this library).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

@@ -103,74 +103,52 @@ struct DecShape {
   static constexpr int kTile = kKeys * kDecWarps;
   static constexpr int kRow = D * (int)sizeof(T) + 16;           // padded row
   static constexpr int kStage = 2 * kKeys * kRow;                // K rows, V rows
-  static constexpr int kSmem = kDecWarps * kDecStages * kStage;
+  static constexpr int kRing = kDecStages * kStage;              // a warp's stages
+  static constexpr int kSmem = kDecWarps * kRing;
 };
 
-template <typename T, int E>
-__device__ __forceinline__ void dec_row(const uint8_t* row, int lane, float (&v)[E]);
-template <>
-__device__ __forceinline__ void dec_row<float, 4>(const uint8_t* row, int lane, float (&v)[4]) {
-  const float4 x = reinterpret_cast<const float4*>(row)[lane];
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-template <>
-__device__ __forceinline__ void dec_row<float, 2>(const uint8_t* row, int lane, float (&v)[2]) {
-  const float2 x = reinterpret_cast<const float2*>(row)[lane];
-  v[0] = x.x; v[1] = x.y;
-}
-template <>
-__device__ __forceinline__ void dec_row<__nv_bfloat16, 4>(const uint8_t* row, int lane,
-                                                          float (&v)[4]) {
-  const uint2 x = reinterpret_cast<const uint2*>(row)[lane];
-  v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
-  v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
-}
-template <>
-__device__ __forceinline__ void dec_row<__nv_bfloat16, 2>(const uint8_t* row, int lane,
-                                                          float (&v)[2]) {
-  const uint32_t x = reinterpret_cast<const uint32_t*>(row)[lane];
-  v[0] = __uint_as_float(x << 16); v[1] = __uint_as_float(x & 0xffff0000u);
-}
+// What a block knows of the line of tiles.
+struct DecLine {
+  long long total, B;   // tiles, blocks that share them
+  long long u0, u1;     // this block's
+};
 
-// Each warp holds D / 32 elements of every row per lane and 8 heads' outputs;
-// its keys pass through a ring of stages of its own in shared memory (cp.async),
-// so warps run without block barriers inside a run.
+struct DecShared {
+  long long warp_sum[kDecWarps];
+  DecSpot first;
+  float m[kDecWarps][kDecHeads], l[kDecWarps][kDecHeads];
+  uint32_t bits[kDecWarps];
+};
+
+// Finds the block's share and its first run; writes the results of sequences
+// without keys. All threads; ends with a barrier.
 template <typename T, int D>
-__global__ void __launch_bounds__(kDecWarps * 32) decode_kernel(const DecodeArgs a) {
+__device__ __forceinline__ DecLine dec_begin(const DecodeArgs& a, DecShared& sh, uint32_t* bits) {
   using S = DecShape<T, D>;
-  constexpr int E = D / 32;
-  constexpr int KK = S::kKeys;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long warp_sum[kDecWarps];
-  __shared__ DecSpot first;
-  __shared__ __align__(16) float pbuf[kDecWarps][KK][kDecHeads];  // read 16 bytes at a time
-  __shared__ float mbuf[kDecWarps][kDecHeads], lbuf[kDecWarps][kDecHeads];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.x;
-  uint32_t bits = 0;
-
   long long before;
-  const long long total = dec_total<S::kTile>(a, warp_sum, &before, &bits);
+  DecLine L;
+  L.total = dec_total<S::kTile>(a, sh.warp_sum, &before, bits);
   // blocks that share the line: each of them has a tile at least
-  const long long B = min((long long)gridDim.x, total);
-  const long long u0 = b < B ? total * b / B : 0, u1 = b < B ? total * (b + 1) / B : 0;
-  if (u0 < u1) {
+  L.B = min((long long)gridDim.x, L.total);
+  L.u0 = b < L.B ? L.total * b / L.B : 0;
+  L.u1 = b < L.B ? L.total * (b + 1) / L.B : 0;
+  if (L.u0 < L.u1) {
     const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
     const int i0 = min(a.n_seqs, (int)threadIdx.x * per), i1 = min(a.n_seqs, i0 + per);
     long long at = before;
     for (int i = i0; i < i1; ++i) {
-      const int len = dec_len(a, i, &bits), tiles = (len + S::kTile - 1) / S::kTile;
+      const int len = dec_len(a, i, bits), tiles = (len + S::kTile - 1) / S::kTile;
       const long long mine = (long long)tiles * a.hkv * a.hgroups;
-      if (u0 >= at && u0 < at + mine) {
-        const int in = (int)(u0 - at);
-        first = DecSpot{i, len, tiles, in / tiles, in % tiles};
+      if (L.u0 >= at && L.u0 < at + mine) {
+        const int in = (int)(L.u0 - at);
+        sh.first = DecSpot{i, len, tiles, in / tiles, in % tiles};
       }
       at += mine;
     }
   }
-  // sequences without keys
   for (int i = b; i < a.n_seqs; i += gridDim.x) {
-    if (dec_len(a, i, &bits) > 0) continue;
+    if (dec_len(a, i, bits) > 0) continue;
     for (int e = threadIdx.x; e < a.hq * D; e += blockDim.x)
       static_cast<T*>(a.out)[(int64_t)i * a.hq * D + e] = from_f32<T>(0.f);
     if (a.lse)
@@ -178,240 +156,498 @@ __global__ void __launch_bounds__(kDecWarps * 32) decode_kernel(const DecodeArgs
         a.lse[(int64_t)i * a.hq + h] = -INFINITY;
   }
   __syncthreads();
-  int4 join = make_int4(-1, 0, 0, 0);
-  if (u0 < u1) {
-    DecSpot at = first;
-    long long u = u0;
-    uint8_t* ring = smem + warp * kDecStages * S::kStage;
-    while (u < u1) {
-      const int n_tiles = (int)min((long long)(at.tiles - at.tile), u1 - u);
-      const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
-      const int heads = min(kDecHeads, a.group - hg * kDecHeads);
-      const int h0 = kvh * a.group + hg * kDecHeads;
-      float q[kDecHeads][E], o[kDecHeads][E];
-      float m[kDecHeads / 8], l = 0.f;   // this lane's head: lane % 8
-      m[0] = -INFINITY;
-#pragma unroll
-      for (int h = 0; h < kDecHeads; ++h) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          q[h][e] = 0.f;
-          o[h][e] = 0.f;
-        }
-        if (h < heads) {
-          const T* p = static_cast<const T*>(a.q) + at.seq * a.qs.ts + (h0 + h) * a.qs.hs;
-#pragma unroll
-          for (int e = 0; e < E; ++e) q[h][e] = to_f32(p[lane * E + e]);
-        }
-      }
-      const int32_t* pages = a.table + at.seq * a.table_stride;
-      const int key0 = at.tile * S::kTile + warp * KK;
+  return L;
+}
 
-      // Rows of stage i into the ring: lane r < KK finds row r, then every row is copied by
-      // consecutive lanes. Returns the bits of the rows that are there.
-      auto fetch = [&](int i) -> uint32_t {
-        int64_t off = -1;
-        if (i < n_tiles && lane < KK) {
-          const int key = key0 + i * S::kTile + lane;
-          if (key < at.len) {
-            const int page = pages[key / a.cs.page_size];
-            if (page >= 0 && page < a.cs.n_pages)
-              off = page * a.cs.ps + (key % a.cs.page_size) * a.cs.ts + kvh * a.cs.hs;
-            else
-              bits |= ADASPARK_DEV_BAD_LAYOUT;
-          }
-        }
-        const uint32_t there = __ballot_sync(0xffffffffu, off >= 0);
-        uint8_t* st = ring + (i % kDecStages) * S::kStage;
-        constexpr int per_row = D * (int)sizeof(T) / 16;       // 16-byte pieces of a row
-        constexpr int rows = 32 / per_row > 0 ? 32 / per_row : 1;
-        const int r0 = lane / per_row, piece = lane % per_row;
-        if (i < n_tiles) {
-#pragma unroll
-          for (int r = 0; r < KK; r += rows) {
-            const int64_t ro = __shfl_sync(0xffffffffu, off, r + r0);
-            const bool ok = ro >= 0;
-            const int64_t eo = ok ? ro : 0;
-            cp_async16(st + (r + r0) * S::kRow + piece * 16,
-                       reinterpret_cast<const uint8_t*>(static_cast<const T*>(a.kc) + eo) +
-                           piece * 16, ok);
-            cp_async16(st + (KK + r + r0) * S::kRow + piece * 16,
-                       reinterpret_cast<const uint8_t*>(static_cast<const T*>(a.vc) + eo) +
-                           piece * 16, ok);
-          }
-        }
-        cp_async_commit();
-        return there;
-      };
+// Element offset of a key's row in the cache, -1 for a key that is not there.
+// `page` is the table's entry for the key (any value where key >= len).
+__device__ __forceinline__ int64_t dec_offset(const DecodeArgs& a, int key, int len, int page,
+                                              int kvh, uint32_t* bits) {
+  if (key >= len) return -1;
+  if (page < 0 || page >= a.cs.n_pages) {
+    *bits |= ADASPARK_DEV_BAD_LAYOUT;
+    return -1;
+  }
+  return page * a.cs.ps + (key % a.cs.page_size) * a.cs.ts + kvh * a.cs.hs;
+}
 
-      uint32_t there[kDecStages];
+// Copies a stage's rows, row r at lane r's offset: consecutive lanes take the
+// 16-byte pieces of a row. One commit group, empty when nothing is wanted.
+template <typename T, int D>
+__device__ __forceinline__ void dec_copy(const DecodeArgs& a, uint8_t* st, int64_t off, bool want) {
+  using S = DecShape<T, D>;
+  constexpr int per_row = D * (int)sizeof(T) / 16, rows = 32 / per_row;
+  const int lane = threadIdx.x & 31, r0 = lane / per_row, piece = lane % per_row;
+  if (want) {
 #pragma unroll
-      for (int i = 0; i < kDecStages - 1; ++i) there[i] = fetch(i);
-      for (int i = 0; i < n_tiles; ++i) {
-        __syncwarp();  // the stage that is fetched into was read by every lane
-        const uint32_t next = fetch(i + kDecStages - 1);
-        cp_async_wait<kDecStages - 1>();
-        __syncwarp();
-        const uint32_t here = there[0];
+    for (int r = 0; r < S::kKeys; r += rows) {
+      const int64_t ro = __shfl_sync(0xffffffffu, off, r + r0);
+      const bool ok = ro >= 0;
+      const int64_t byte = (ok ? ro * (int)sizeof(T) : 0) + piece * 16;
+      cp_async16(st + (r + r0) * S::kRow + piece * 16, static_cast<const uint8_t*>(a.kc) + byte, ok);
+      cp_async16(st + (S::kKeys + r + r0) * S::kRow + piece * 16,
+                 static_cast<const uint8_t*>(a.vc) + byte, ok);
+    }
+  }
+  cp_async_commit();
+}
+
+// Joins the warps' parts of a run (maxima and sums in sh, outputs [8][D] at the
+// start of each warp's ring) and writes its results or the block's partial ones.
+// All threads; the caller puts a barrier before and after. Returns the joins
+// entry of a cut run that starts in this block.
+template <typename T, int D>
+__device__ __forceinline__ void dec_end_run(const DecodeArgs& a, const DecShared& sh,
+                                            const uint8_t* smem, const DecSpot& at, int n_tiles,
+                                            long long u, const DecLine& L, int4* join) {
+  using S = DecShape<T, D>;
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
+  const int heads = min(kDecHeads, a.group - hg * kDecHeads);
+  const int h0 = kvh * a.group + hg * kDecHeads;
+  const bool whole = at.tile == 0 && n_tiles == at.tiles;
+  const int slot = 2 * blockIdx.x + (u == L.u0 ? 0 : 1);
+  for (int h = warp; h < heads; h += kDecWarps) {
+    float mm = -INFINITY;
 #pragma unroll
-        for (int k = 0; k + 1 < kDecStages - 1; ++k) there[k] = there[k + 1];
-        there[kDecStages - 2] = next;
-        const uint8_t* st = ring + (i % kDecStages) * S::kStage;
-        // scores, four keys at a time; lane = key * 8 + head holds one of the 32 sums
-        float z[KK / 4];
-        float top = -INFINITY;
+    for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, sh.m[w][h]);
+    const float mu = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, acc[E] = {};
 #pragma unroll
-        for (int g = 0; g < KK / 4; ++g) {
-          float d[32];
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float f = exp2f(sh.m[w][h] - mu);
+      ll = fmaf(sh.l[w][h], f, ll);
+      const float* ob = reinterpret_cast<const float*>(smem + w * S::kRing);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float x[E];
-            dec_row<T, E>(st + (4 * g + k) * S::kRow, lane, x);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(ob[h * D + lane * E + e], f, acc[e]);
+    }
+    if (whole) {
+      const float r = 1.f / ll;
+      T* op = static_cast<T*>(a.out) + ((int64_t)at.seq * a.hq + h0 + h) * D + lane * E;
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-              float acc = 0.f;
+      for (int e = 0; e < E; ++e) op[e] = from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
+      if (a.lse && lane == 0)
+        a.lse[(int64_t)at.seq * a.hq + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    } else {
+      float* pp = a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
 #pragma unroll
-              for (int e = 0; e < E; ++e) acc = fmaf(q[h][e], x[e], acc);
-              d[k * 8 + h] = acc;
-            }
-          }
-          // halve the values while folding the lanes: lane bit w keeps the half with that bit
-#pragma unroll
-          for (int w = 16; w >= 1; w >>= 1) {
-#pragma unroll
-            for (int j = 0; j < w; ++j) {
-              const bool up = lane & w;
-              const float keep = up ? d[j + w] : d[j], give = up ? d[j] : d[j + w];
-              d[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-            }
-          }
-          const bool ok = here >> (4 * g + (lane >> 3)) & 1;
-          z[g] = ok ? d[0] * a.scale_log2 : -INFINITY;
-          top = fmaxf(top, z[g]);
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        const float m_new = fmaxf(m[0], top);
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m[0] - m_use);
-        m[0] = m_new;
-        l *= alpha;
-#pragma unroll
-        for (int g = 0; g < KK / 4; ++g) {
-          const float p = exp2f(z[g] - m_use);
-          l += p;
-          pbuf[warp][4 * g + (lane >> 3)][lane & 7] = p;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const float f = __shfl_sync(0xffffffffu, alpha, h);
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[h][e] *= f;
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-          float x[E];
-          dec_row<T, E>(st + (KK + k) * S::kRow, lane, x);
-          const float4 pa = *reinterpret_cast<const float4*>(&pbuf[warp][k][0]);
-          const float4 pb = *reinterpret_cast<const float4*>(&pbuf[warp][k][4]);
-          const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-#pragma unroll
-          for (int h = 0; h < 8; ++h)
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[h][e] = fmaf(p[h], x[e], o[h][e]);
-        }
-      }
-      cp_async_wait<0>();
-      // join the warps: sums over the lanes of a head, then over the warps
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (lane < 8) {
-        mbuf[warp][lane] = m[0];
-        lbuf[warp][lane] = l;
-      }
-      float* obuf = reinterpret_cast<float*>(ring);  // [8][D]: this warp's ring is at rest
-      __syncwarp();
-#pragma unroll
-      for (int h = 0; h < 8; ++h)
-#pragma unroll
-        for (int e = 0; e < E; ++e) obuf[h * D + lane * E + e] = o[h][e];
-      __syncthreads();
-      const bool whole = at.tile == 0 && n_tiles == at.tiles;
-      const int slot = 2 * b + (u == u0 ? 0 : 1);
-      for (int h = warp; h < heads; h += kDecWarps) {
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, mbuf[w][h]);
-        const float mu = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f, acc[E] = {};
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float f = exp2f(mbuf[w][h] - mu);
-          ll = fmaf(lbuf[w][h], f, ll);
-          const float* ob = reinterpret_cast<const float*>(smem + w * kDecStages * S::kStage);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(ob[h * D + lane * E + e], f, acc[e]);
-        }
-        if (whole) {
-          const float r = ll == 0.f ? 0.f : 1.f / ll;
-          T* op = static_cast<T*>(a.out) + ((int64_t)at.seq * a.hq + h0 + h) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) op[e] = from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
-          if (a.lse && lane == 0)
-            a.lse[(int64_t)at.seq * a.hq + h0 + h] =
-                ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-        } else {
-          float* pp = a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
-#pragma unroll
-          for (int e = 0; e < E; ++e) pp[lane * E + e] = acc[e];
-          if (lane == 0) {
-            pp[D] = mm;
-            pp[D + 1] = ll;
-          }
-        }
-      }
-      __syncthreads();
-      if (!whole && at.tile == 0) {
-        // the first block of a cut run: its parts are this slot and the first slots of the
-        // blocks up to the one that holds the run's last tile
-        const long long end = u + at.tiles - 1;
-        long long last = end * B / total;
-        while (total * (last + 1) / B <= end) ++last;
-        while (total * last / B > end) --last;
-        join = make_int4(at.seq, at.run, slot, 2 * (int)last);
-      }
-      u += n_tiles;
-      at.tile = 0;
-      if (++at.run == a.hkv * a.hgroups) {
-        at.run = 0;
-        do {
-          ++at.seq;
-          if (at.seq >= a.n_seqs) break;
-          at.len = dec_len(a, at.seq, &bits);
-          at.tiles = (at.len + S::kTile - 1) / S::kTile;
-        } while (at.tiles == 0);
+      for (int e = 0; e < E; ++e) pp[lane * E + e] = acc[e];
+      if (lane == 0) {
+        pp[D] = mm;
+        pp[D + 1] = ll;
       }
     }
   }
+  if (!whole && at.tile == 0) {
+    // the first block of a cut run: its parts are this slot and the first slots of the
+    // blocks up to the one that holds the run's last tile
+    const long long end = u + at.tiles - 1;
+    long long last = end * L.B / L.total;
+    while (L.total * (last + 1) / L.B <= end) ++last;
+    while (L.total * last / L.B > end) --last;
+    *join = make_int4(at.seq, at.run, slot, 2 * (int)last);
+  }
+}
+
+// Next run on the line.
+template <int TILE>
+__device__ __forceinline__ void dec_advance(const DecodeArgs& a, DecSpot* at, uint32_t* bits) {
+  at->tile = 0;
+  if (++at->run < a.hkv * a.hgroups) return;
+  at->run = 0;
+  do {
+    if (++at->seq >= a.n_seqs) return;
+    at->len = dec_len(a, at->seq, bits);
+    at->tiles = (at->len + TILE - 1) / TILE;
+  } while (at->tiles == 0);
+}
+
+__device__ __forceinline__ void dec_end(const DecodeArgs& a, DecShared& sh, uint32_t bits,
+                                        int4 join) {
   bits = __reduce_or_sync(0xffffffffu, bits);
-  __shared__ uint32_t all_bits[kDecWarps];
-  if (lane == 0) all_bits[warp] = bits;
+  if ((threadIdx.x & 31) == 0) sh.bits[threadIdx.x >> 5] = bits;
   __syncthreads();
   if (threadIdx.x == 0) {
     uint32_t v = 0;
-    for (int w = 0; w < kDecWarps; ++w) v |= all_bits[w];
-    a.status[b] = (int32_t)v;
-    a.joins[b] = join;
+    for (int w = 0; w < kDecWarps; ++w) v |= sh.bits[w];
+    a.status[blockIdx.x] = (int32_t)v;
+    a.joins[blockIdx.x] = join;
   }
+}
+
+template <int E>
+__device__ __forceinline__ void dec_row(const uint8_t* row, int lane, float (&v)[E]);
+template <>
+__device__ __forceinline__ void dec_row<4>(const uint8_t* row, int lane, float (&v)[4]) {
+  const float4 x = reinterpret_cast<const float4*>(row)[lane];
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+template <>
+__device__ __forceinline__ void dec_row<2>(const uint8_t* row, int lane, float (&v)[2]) {
+  const float2 x = reinterpret_cast<const float2*>(row)[lane];
+  v[0] = x.x; v[1] = x.y;
+}
+
+// fp32: each lane holds D / 32 elements of every row and of 8 heads' outputs; a
+// warp's keys pass through a ring of stages of its own in shared memory
+// (cp.async), so warps run without block barriers inside a run.
+template <int D>
+__global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(const DecodeArgs a) {
+  using T = float;
+  using S = DecShape<T, D>;
+  constexpr int E = D / 32, KK = S::kKeys;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ DecShared sh;
+  __shared__ __align__(16) float pbuf[kDecWarps][KK][kDecHeads];  // read 16 bytes at a time
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  dependency_release();
+  uint32_t bits = 0;
+  const DecLine L = dec_begin<T, D>(a, sh, &bits);
+  int4 join = make_int4(-1, 0, 0, 0);
+  DecSpot at = sh.first;
+  uint8_t* ring = smem + warp * S::kRing;
+  for (long long u = L.u0; u < L.u1;) {
+    const int n_tiles = (int)min((long long)(at.tiles - at.tile), L.u1 - u);
+    const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
+    const int heads = min(kDecHeads, a.group - hg * kDecHeads);
+    const int h0 = kvh * a.group + hg * kDecHeads;
+    float q[kDecHeads][E], o[kDecHeads][E];
+    float m = -INFINITY, l = 0.f;   // this lane's head: lane % 8
+#pragma unroll
+    for (int h = 0; h < kDecHeads; ++h) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        q[h][e] = 0.f;
+        o[h][e] = 0.f;
+      }
+      if (h < heads) {
+        const T* p = static_cast<const T*>(a.q) + at.seq * a.qs.ts + (h0 + h) * a.qs.hs;
+#pragma unroll
+        for (int e = 0; e < E; ++e) q[h][e] = p[lane * E + e];
+      }
+    }
+    const int32_t* pages = a.table + at.seq * a.table_stride;
+    const int key0 = at.tile * S::kTile + warp * KK;
+
+    // Rows of stage i into the ring; returns the bits of the rows that are there.
+    auto fetch = [&](int i) -> uint32_t {
+      const int key = key0 + i * S::kTile + lane;
+      int64_t off = -1;
+      if (i < n_tiles && lane < KK && key < at.len)
+        off = dec_offset(a, key, at.len, pages[key / a.cs.page_size], kvh, &bits);
+      dec_copy<T, D>(a, ring + (i % kDecStages) * S::kStage, off, i < n_tiles);
+      return __ballot_sync(0xffffffffu, off >= 0);
+    };
+
+    uint32_t there[kDecStages];
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) there[i] = fetch(i);
+    for (int i = 0; i < n_tiles; ++i) {
+      __syncwarp();  // the stage that is fetched into was read by every lane
+      const uint32_t next = fetch(i + kDecStages - 1);
+      cp_async_wait<kDecStages - 1>();
+      __syncwarp();
+      const uint32_t here = there[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kDecStages - 1; ++k) there[k] = there[k + 1];
+      there[kDecStages - 2] = next;
+      const uint8_t* st = ring + (i % kDecStages) * S::kStage;
+      // scores, four keys at a time; lane = key * 8 + head holds one of the 32 sums
+      float z[KK / 4];
+      float top = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < KK / 4; ++g) {
+        float d[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float x[E];
+          dec_row<E>(st + (4 * g + k) * S::kRow, lane, x);
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            float acc = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc = fmaf(q[h][e], x[e], acc);
+            d[k * 8 + h] = acc;
+          }
+        }
+        // halve the values while folding the lanes: lane bit w keeps the half with that bit
+#pragma unroll
+        for (int w = 16; w >= 1; w >>= 1) {
+#pragma unroll
+          for (int j = 0; j < w; ++j) {
+            const bool up = lane & w;
+            const float keep = up ? d[j + w] : d[j], give = up ? d[j] : d[j + w];
+            d[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+          }
+        }
+        const bool ok = here >> (4 * g + (lane >> 3)) & 1;
+        z[g] = ok ? d[0] * a.scale_log2 : -INFINITY;
+        top = fmaxf(top, z[g]);
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float m_new = fmaxf(m, top);
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m - m_use);
+      m = m_new;
+      l *= alpha;
+#pragma unroll
+      for (int g = 0; g < KK / 4; ++g) {
+        const float p = exp2f(z[g] - m_use);
+        l += p;
+        pbuf[warp][4 * g + (lane >> 3)][lane & 7] = p;
+      }
+      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const float f = __shfl_sync(0xffffffffu, alpha, h);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[h][e] *= f;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < KK; ++k) {
+        float x[E];
+        dec_row<E>(st + (KK + k) * S::kRow, lane, x);
+        const float4 pa = *reinterpret_cast<const float4*>(&pbuf[warp][k][0]);
+        const float4 pb = *reinterpret_cast<const float4*>(&pbuf[warp][k][4]);
+        const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+        for (int h = 0; h < 8; ++h)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[h][e] = fmaf(p[h], x[e], o[h][e]);
+      }
+    }
+    cp_async_wait<0>();
+    l += __shfl_xor_sync(0xffffffffu, l, 8);
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (lane < 8) {
+      sh.m[warp][lane] = m;
+      sh.l[warp][lane] = l;
+    }
+    __syncwarp();
+    float* obuf = reinterpret_cast<float*>(ring);  // this warp's ring is at rest
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+#pragma unroll
+      for (int e = 0; e < E; ++e) obuf[h * D + lane * E + e] = o[h][e];
+    __syncthreads();
+    dec_end_run<T, D>(a, sh, smem, at, n_tiles, u, L, &join);
+    __syncthreads();
+    u += n_tiles;
+    dec_advance<S::kTile>(a, &at, &bits);
+  }
+  dec_end(a, sh, bits, join);
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const uint8_t* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], const uint8_t* p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+// Transpose of an 8x8 matrix of 16-bit elements held by the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// c [16 x 8] += A [16 x 16] B [16 x 8], bf16 in, fp32 accumulation.
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// bf16: keys fill the rows of a product's tile and 8 query heads its columns,
+//   S^T [16 keys x 8 heads] = K Q^T,   O^T [16 d x 8 heads] += V^T P^T,
+// so that no part of a tile is padding when a KV head serves 8 query heads (128
+// rows of tcgen05 would hold 7 or 8 of them), and a lane's softmax columns are
+// its output columns. P goes to the second product as two bf16 parts (high and
+// rest: 2^-17 relative), which costs 8 more products per 16 keys and keeps the
+// output as near as fp32 weights would. The warp's keys pass through a ring of
+// stages of its own (cp.async), the table entry of a stage one step ahead.
+template <int D>
+__global__ void __launch_bounds__(kDecWarps * 32) decode_mma_kernel(const DecodeArgs a) {
+  using T = __nv_bfloat16;
+  using S = DecShape<T, D>;
+  constexpr int KK = S::kKeys, MT = KK / 16, DT = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ DecShared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  dependency_release();
+  uint32_t bits = 0;
+  const DecLine L = dec_begin<T, D>(a, sh, &bits);
+  int4 join = make_int4(-1, 0, 0, 0);
+  DecSpot at = sh.first;
+  uint8_t* ring = smem + warp * S::kRing;
+  for (long long u = L.u0; u < L.u1;) {
+    const int n_tiles = (int)min((long long)(at.tiles - at.tile), L.u1 - u);
+    const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
+    const int heads = min(kDecHeads, a.group - hg * kDecHeads);
+    const int h0 = kvh * a.group + hg * kDecHeads;
+    const int32_t* pages = a.table + at.seq * a.table_stride;
+    const int key0 = at.tile * S::kTile + warp * KK + lane;  // of this lane's row, stage 0
+    auto entry = [&](int i) -> int {
+      const int key = key0 + i * S::kTile;
+      return i < n_tiles && lane < KK && key < at.len ? pages[key / a.cs.page_size] : 0;
+    };
+    auto fetch = [&](int i, int page) -> uint32_t {
+      const int64_t off = i < n_tiles && lane < KK
+                              ? dec_offset(a, key0 + i * S::kTile, at.len, page, kvh, &bits)
+                              : -1;
+      dec_copy<T, D>(a, ring + (i % kDecStages) * S::kStage, off, i < n_tiles);
+      return __ballot_sync(0xffffffffu, off >= 0);
+    };
+    uint32_t there[kDecStages];
+    int page[kDecStages];
+#pragma unroll
+    for (int i = 0; i < kDecStages; ++i) page[i] = entry(i);
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) there[i] = fetch(i, page[i]);
+    int ahead = page[kDecStages - 1];
+    // Q^T: column g is head g, rows 2c, 2c + 1 and 8 further of each 16 of d
+    uint32_t qf[DT][2];
+#pragma unroll
+    for (int k = 0; k < DT; ++k) {
+      qf[k][0] = qf[k][1] = 0u;
+      if (g < heads) {
+        const T* p = static_cast<const T*>(a.q) + at.seq * a.qs.ts + (h0 + g) * a.qs.hs + 16 * k +
+                     2 * c;
+        qf[k][0] = *reinterpret_cast<const uint32_t*>(p);
+        qf[k][1] = *reinterpret_cast<const uint32_t*>(p + 8);
+      }
+    }
+    float o[DT][4];
+#pragma unroll
+    for (int k = 0; k < DT; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
+
+    for (int i = 0; i < n_tiles; ++i) {
+      __syncwarp();  // the stage that is fetched into was read by every lane
+      const uint32_t next = fetch(i + kDecStages - 1, ahead);
+      ahead = entry(i + kDecStages);
+      cp_async_wait<kDecStages - 1>();
+      __syncwarp();
+      const uint32_t here = there[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kDecStages - 1; ++k) there[k] = there[k + 1];
+      there[kDecStages - 2] = next;
+      const uint8_t* st = ring + (i % kDecStages) * S::kStage;
+      // scores: rows g and g + 8 of each 16 keys, heads 2c and 2c + 1
+      float z[MT][4];
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        float s0[4] = {}, s1[4] = {};  // even and odd steps: two shorter chains
+        const uint8_t* row = st + (16 * t + (lane & 15)) * S::kRow + (lane >> 4) * 16;
+#pragma unroll
+        for (int k = 0; k < DT; ++k) {
+          uint32_t f[4];
+          ldmatrix4(f, row + k * 32);
+          if (k & 1)
+            mma_16816(s1, f, qf[k][0], qf[k][1]);
+          else
+            mma_16816(s0, f, qf[k][0], qf[k][1]);
+        }
+        const bool lo = here >> (16 * t + g) & 1, hi = here >> (16 * t + g + 8) & 1;
+        z[t][0] = lo ? (s0[0] + s1[0]) * a.scale_log2 : -INFINITY;
+        z[t][1] = lo ? (s0[1] + s1[1]) * a.scale_log2 : -INFINITY;
+        z[t][2] = hi ? (s0[2] + s1[2]) * a.scale_log2 : -INFINITY;
+        z[t][3] = hi ? (s0[3] + s1[3]) * a.scale_log2 : -INFINITY;
+        t0 = fmaxf(t0, fmaxf(z[t][0], z[t][2]));
+        t1 = fmaxf(t1, fmaxf(z[t][1], z[t][3]));
+      }
+#pragma unroll
+      for (int w = 4; w <= 16; w <<= 1) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+      }
+      t0 = fmaxf(t0, m0);
+      t1 = fmaxf(t1, m1);
+      const float u0 = t0 == -INFINITY ? 0.f : t0, u1 = t1 == -INFINITY ? 0.f : t1;
+      if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {
+        const float f0 = exp2f(m0 - u0), f1 = exp2f(m1 - u1);
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int k = 0; k < DT; ++k) {
+          o[k][0] *= f0; o[k][1] *= f1; o[k][2] *= f0; o[k][3] *= f1;
+        }
+        m0 = t0;
+        m1 = t1;
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const float p0 = exp2f(z[t][0] - u0), p1 = exp2f(z[t][1] - u1);
+        const float p2 = exp2f(z[t][2] - u0), p3 = exp2f(z[t][3] - u1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        const uint32_t ha = pack_bf16x2(p0, p1), hb = pack_bf16x2(p2, p3);
+        const uint32_t ra = pack_bf16x2(p0 - __uint_as_float(ha << 16),
+                                        p1 - __uint_as_float(ha & 0xffff0000u));
+        const uint32_t rb = pack_bf16x2(p2 - __uint_as_float(hb << 16),
+                                        p3 - __uint_as_float(hb & 0xffff0000u));
+        const uint32_t ph0 = movmatrix(ha), ph1 = movmatrix(hb);
+        const uint32_t pr0 = movmatrix(ra), pr1 = movmatrix(rb);
+        const uint8_t* row = st + (KK + 16 * t + (lane & 7) + (lane >> 4) * 8) * S::kRow +
+                             (lane >> 3 & 1) * 16;
+#pragma unroll
+        for (int k = 0; k < DT; ++k) {
+          uint32_t f[4];
+          ldmatrix4_trans(f, row + k * 32);
+          mma_16816(o[k], f, ph0, ph1);
+          mma_16816(o[k], f, pr0, pr1);
+        }
+      }
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int w = 4; w <= 16; w <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+    }
+    if (g == 0) {
+      sh.m[warp][2 * c] = m0;
+      sh.m[warp][2 * c + 1] = m1;
+      sh.l[warp][2 * c] = l0;
+      sh.l[warp][2 * c + 1] = l1;
+    }
+    __syncwarp();
+    float* obuf = reinterpret_cast<float*>(ring);  // this warp's ring is at rest
+#pragma unroll
+    for (int k = 0; k < DT; ++k) {
+      obuf[2 * c * D + 16 * k + g] = o[k][0];
+      obuf[(2 * c + 1) * D + 16 * k + g] = o[k][1];
+      obuf[2 * c * D + 16 * k + g + 8] = o[k][2];
+      obuf[(2 * c + 1) * D + 16 * k + g + 8] = o[k][3];
+    }
+    __syncthreads();
+    dec_end_run<T, D>(a, sh, smem, at, n_tiles, u, L, &join);
+    __syncthreads();
+    u += n_tiles;
+    dec_advance<S::kTile>(a, &at, &bits);
+  }
+  dec_end(a, sh, bits, join);
 }
 
 // Joins the parts of a run that was cut: one block per block of the first kernel (the run
 // that starts there and ends in a later one) and head. Block (0, 0) collects the status.
 template <typename T, int D>
 __global__ void __launch_bounds__(D) decode_join_kernel(const DecodeArgs a, int B) {
+  dependency_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
     uint32_t v = 0;
     for (int i = threadIdx.x; i < B; i += 32) v |= (uint32_t)a.status[i];
@@ -465,10 +701,11 @@ DecLayout dec_layout(int d) {
 }
 
 template <typename T, int D>
-cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_decode(const DecodeArgs& a, void (*kernel)(DecodeArgs), int sms,
+                          cudaStream_t s) {
   using S = DecShape<T, D>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   // no more blocks than tiles the tables can hold
   const int64_t tiles = (int64_t)a.n_seqs * a.hkv * a.hgroups *
@@ -476,12 +713,12 @@ cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
   int64_t grid = 2 * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;
   if (grid > tiles) grid = tiles;
-  e = launch("decode_attn", decode_kernel<T, D>, dim3((unsigned)grid), dim3(kDecWarps * 32),
-             S::kSmem, s, a);
-  if (e != cudaSuccess) return e;
+  const cudaError_t r = launch("decode_attn", kernel, dim3((unsigned)grid), dim3(kDecWarps * 32),
+                               S::kSmem, s, a);
+  if (r != cudaSuccess) return r;
   const int heads = a.group < kDecHeads ? a.group : kDecHeads;
-  return launch("decode_join", decode_join_kernel<T, D>, dim3((unsigned)grid, heads), dim3(D), 0, s,
-                a, (int)grid);
+  return launch_after("decode_join", decode_join_kernel<T, D>, dim3((unsigned)grid, heads), dim3(D),
+                      0, s, a, (int)grid);
 }
 
 }  // namespace
@@ -534,10 +771,11 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   a.part = reinterpret_cast<float*>(ws + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == ADASPARK_BF16)
-    return cuda_status(d == 128 ? launch_decode<__nv_bfloat16, 128>(a, sms, s)
-                                : launch_decode<__nv_bfloat16, 64>(a, sms, s));
-  return cuda_status(d == 128 ? launch_decode<float, 128>(a, sms, s)
-                              : launch_decode<float, 64>(a, sms, s));
+    return cuda_status(
+        d == 128 ? launch_decode<__nv_bfloat16, 128>(a, decode_mma_kernel<128>, sms, s)
+                 : launch_decode<__nv_bfloat16, 64>(a, decode_mma_kernel<64>, sms, s));
+  return cuda_status(d == 128 ? launch_decode<float, 128>(a, decode_simt_kernel<128>, sms, s)
+                              : launch_decode<float, 64>(a, decode_simt_kernel<64>, sms, s));
 }
 
 }  // extern "C"

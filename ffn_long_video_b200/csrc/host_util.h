@@ -29,6 +29,30 @@ inline cudaError_t launch(const char* name, void (*kernel)(KArgs...), dim3 grid,
   count_launch();
   return e;
 }
+
+// launch() of a kernel whose blocks may come up while the stream's previous
+// kernel still runs: it must call dependency_wait() (common.cuh) before it
+// touches anything that kernel writes.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_after(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                                size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  timer_begin(name, s);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  timer_end(s);
+  count_launch();
+  return e;
+}
 #endif
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
