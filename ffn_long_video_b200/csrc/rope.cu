@@ -13,9 +13,7 @@
 // Memory-bound: every element is read and written once. d/16 lanes own a head,
 // two runs of 8 elements each (16-byte accesses in bf16): the runs of a rotated
 // lane hold both halves of its pairs in either layout, so the rotation needs no
-// exchange, and the norm's sum takes log2(d/16) shuffles. The warp's groups of
-// lanes share one token's angles: each lane computes 8 / groups of them and the
-// warp exchanges them by shuffles. Angles are reduced to a turn in 64 bits
+// exchange, and the norm's sum takes log2(d/16) shuffles. Angles are reduced to a turn in 64 bits
 // (positions of 2^20 and more keep full fp32 accuracy), sines and cosines, norms
 // and rotations are in 32 bits and outputs rounded once.
 #include <cmath>
@@ -42,86 +40,115 @@ struct RopeArgs {
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-template <int D>
+// Forward: runs of 8 elements and blocks that stay, 7 of them on an SM for bf16
+// (70 registers). 65792 tokens of 28 + 4 heads of 128, with the caches read cold:
+// 163 us at 7, 177 at 8 (spills), 190 for blocks that end after a token; runs of
+// 4 elements 212. 18559 normalised tokens of 16 + 2 heads: 34, 36, 38 and 42 us.
+constexpr int kRopeRun = 8;
+template <typename T>
+constexpr int kRopeBlocks = sizeof(T) == 2 ? 7 : 5;
+// Backward: 5 blocks per SM. 18560 tokens of 16 + 2 normalised heads: 73 us at 5,
+// 79 at 4, 98 at 6 and 113 at 8 (spills); 154 before the next step's rows were
+// loaded ahead.
+constexpr int kBwdBlocksPerSm = 5;
+
+// A head's lanes, each with two runs of V elements.
+template <int D, int V>
 struct RopeMap {
-  static constexpr int kLanes = D / 16;          // lanes per head
+  static constexpr int kLanes = D / (2 * V);     // lanes per head
   static constexpr int kHeads = 32 / kLanes;     // heads per warp step
-  static constexpr int kAngles = 8 / kHeads > 0 ? 8 / kHeads : 1;  // angles a lane computes
+  static constexpr int kAngles = V / kHeads;     // angles a lane computes
+  static_assert(kAngles >= 1, "");
 };
 
-// First elements of the two 8-element runs of lane `l` of a head.
+// First elements of the two runs of lane `l` of a head.
+template <int V>
 __device__ __forceinline__ void rope_runs(int l, int rot, int* e0, int* e1) {
-  const int rl = rot >> 4;  // rotated lanes
+  const int rl = rot / (2 * V);  // rotated lanes
   if (l < rl) {
-    *e0 = 8 * l;
-    *e1 = 8 * l + (rot >> 1);
+    *e0 = V * l;
+    *e1 = V * l + (rot >> 1);
   } else {
-    *e0 = rot + 16 * (l - rl);
-    *e1 = *e0 + 8;
+    *e0 = rot + 2 * V * (l - rl);
+    *e1 = *e0 + V;
   }
 }
 
-// Pair index of entry e (0..7) of a rotated lane's eight pairs.
-template <bool IL>
+// Pair index of entry e of a rotated lane's V pairs.
+template <bool IL, int V>
 __device__ __forceinline__ int rope_pair(int l, int e, int rot) {
-  if (!IL) return 8 * l + e;
-  return e < 4 ? 4 * l + e : 4 * l + (rot >> 2) + (e - 4);
+  if (!IL) return V * l + e;
+  return e < V / 2 ? V / 2 * l + e : V / 2 * l + (rot >> 2) + (e - V / 2);
 }
 
-// cos and sin (times the magnitude) of a token's eight pairs for this lane;
-// 1 and 0 for a lane outside the rotated part.
-template <int D, bool IL>
-__device__ __forceinline__ void rope_angles(const RopeArgs& a, int t, int lane, float (&c)[8],
-                                            float (&s)[8]) {
-  using M = RopeMap<D>;
-  const int l = lane % M::kLanes, grp = lane / M::kLanes;
-  const bool turns = l < (a.rot >> 4);
-  float mc[M::kAngles], ms[M::kAngles];
-#pragma unroll
-  for (int i = 0; i < M::kAngles; ++i) {
-    mc[i] = 1.f;
-    ms[i] = 0.f;
-    if (turns) {
-      const int pair = rope_pair<IL>(l, grp * M::kAngles + i, a.rot);
-      const int axis = pair < a.sec0 ? 0 : pair < a.sec01 ? 1 : 2;
-      const double turn = (double)a.pos[axis * a.pos_axis + t] * a.freq[pair] * kInvTwoPi;
-      float sn, cn;
-      sincospif(2.f * (float)(turn - rint(turn)), &sn, &cn);
-      mc[i] = cn * a.magnitude;
-      ms[i] = sn * a.magnitude;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int src = (e / M::kAngles) * M::kLanes + l;
-    c[e] = __shfl_sync(0xffffffffu, mc[e % M::kAngles], src);
-    s[e] = __shfl_sync(0xffffffffu, ms[e % M::kAngles], src);
-  }
-}
+// The rotation of one token for this lane's V pairs, as factors of element pairs.
+// The lanes of the warp that stand at the same place of different heads share
+// their angles: each computes V / heads of them and the warp exchanges them.
+// Lanes outside the rotated part hold the identity. BACK: the transpose.
+template <int D, bool IL, int V>
+struct RopeTurn {
+  using M = RopeMap<D, V>;
+  // halves: c, s, -s of elements (2i, 2i + 1); interleaved: (c, c) and (-s, s) of pair i
+  F2 c[IL ? V : V / 2], s[IL ? V : V / 2], ns[IL ? 1 : V / 2];
 
-// Rotates a lane's two runs in place (sign = -1 for the transpose).
-template <bool IL>
-__device__ __forceinline__ void rope_turn(float (&u)[8], float (&v)[8], const float (&c)[8],
-                                          const float (&s)[8], float sign) {
-  if (!IL) {
+  template <bool BACK>
+  __device__ __forceinline__ void set(const RopeArgs& a, int t, int lane) {
+    const int l = lane % M::kLanes, grp = lane / M::kLanes;
+    float mc[M::kAngles], ms[M::kAngles];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = u[e], y = v[e], sn = sign * s[e];
-      u[e] = x * c[e] - y * sn;
-      v[e] = y * c[e] + x * sn;
+    for (int i = 0; i < M::kAngles; ++i) {
+      mc[i] = 1.f;
+      ms[i] = 0.f;
+      if (l < a.rot / (2 * V)) {
+        const int pair = rope_pair<IL, V>(l, grp * M::kAngles + i, a.rot);
+        const int axis = pair < a.sec0 ? 0 : pair < a.sec01 ? 1 : 2;
+        const double turn = (double)a.pos[axis * a.pos_axis + t] * a.freq[pair] * kInvTwoPi;
+        float sn, cn;
+        sincospif(2.f * (float)(turn - rint(turn)), &sn, &cn);
+        mc[i] = cn * a.magnitude;
+        ms[i] = (BACK ? -sn : sn) * a.magnitude;
+      }
     }
-  } else {
+    float ce[V], se[V];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = u[2 * e], y = u[2 * e + 1], sn = sign * s[e];
-      u[2 * e] = x * c[e] - y * sn;
-      u[2 * e + 1] = y * c[e] + x * sn;
-      const float z = v[2 * e], w = v[2 * e + 1], sm = sign * s[4 + e];
-      v[2 * e] = z * c[4 + e] - w * sm;
-      v[2 * e + 1] = w * c[4 + e] + z * sm;
+    for (int e = 0; e < V; ++e) {
+      const int src = (e / M::kAngles) * M::kLanes + l;
+      ce[e] = __shfl_sync(0xffffffffu, mc[e % M::kAngles], src);
+      se[e] = __shfl_sync(0xffffffffu, ms[e % M::kAngles], src);
+    }
+    if (IL) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        c[e % (IL ? V : V / 2)] = f2(ce[e], ce[e]);
+        s[e % (IL ? V : V / 2)] = f2(-se[e], se[e]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        c[i] = f2(ce[2 * i], ce[2 * i + 1]);
+        s[i] = f2(se[2 * i], se[2 * i + 1]);
+        ns[i % (IL ? 1 : V / 2)] = f2(-se[2 * i], -se[2 * i + 1]);
+      }
     }
   }
-}
+
+  // Rotates a lane's two runs in place.
+  __device__ __forceinline__ void turn(F2 (&u)[V / 2], F2 (&v)[V / 2]) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      if (IL) {
+        const float2 x = unpack(u[i]), y = unpack(v[i]);
+        u[i] = fma2(f2(x.y, x.x), s[i], mul2(u[i], c[i]));
+        v[i] = fma2(f2(y.y, y.x), s[(V / 2 + i) % (IL ? V : V / 2)],
+                    mul2(v[i], c[(V / 2 + i) % (IL ? V : V / 2)]));
+      } else {
+        const F2 x = u[i], y = v[i];
+        u[i] = fma2(y, ns[i % (IL ? 1 : V / 2)], mul2(x, c[i]));
+        v[i] = fma2(x, s[i], mul2(y, c[i]));
+      }
+    }
+  }
+};
 
 template <int LANES>
 __device__ __forceinline__ float head_sum(float v) {
@@ -130,205 +157,265 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// One warp per (token, part of its heads): queries, then keys, then (with a
-// cache) values, which are copied.
-template <typename T, int D, bool IL, bool CACHE>
-__global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a) {
-  using M = RopeMap<D>;
+// Norm weights of queries and keys in fp32, ones where there is none.
+template <typename T, int D>
+__device__ __forceinline__ void rope_weights(const RopeArgs& a, float (&w)[2][D]) {
+  for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+    const T* p = static_cast<const T*>(i < D ? a.wq : a.wk);
+    w[i / D][i % D] = p ? to_f32(p[i % D]) : 1.f;
+  }
+  __syncthreads();
+}
+template <int V>
+__device__ __forceinline__ void load_f2(const float* p, F2 (&v)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(p)[i];
+    v[2 * i] = f2(x.x, x.y);
+    v[2 * i + 1] = f2(x.z, x.w);
+  }
+}
+
+// Warps walk items (token, part of its heads): queries, then keys, then (with a
+// cache) values, which are copied. The next step's rows, of the next item too,
+// are on their way while a step is computed.
+template <typename T, int D, bool IL, bool CACHE, bool NORM>
+__global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_kernel(const RopeArgs a) {
+  constexpr int V = kRopeRun;
+  using M = RopeMap<D, V>;
+  __shared__ __align__(16) float weights[2][NORM ? D : 1];
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(item / a.parts), part = (int)(item % a.parts);
-  if (t >= a.n) return;
   const int l = lane % M::kLanes, grp = lane / M::kLanes;
   const int heads = a.hq + a.hkv * (CACHE ? 2 : 1);
   const int steps = (heads + M::kHeads - 1) / M::kHeads;
   const int per = (steps + a.parts - 1) / a.parts;
-  const int s0 = part * per, s1 = min(steps, s0 + per);
+  const int items = a.n * a.parts, stride = gridDim.x * 4;
   int e0, e1;
-  rope_runs(l, a.rot, &e0, &e1);
-  float c[8], s[8];
-  if (a.rot > 0) rope_angles<D, IL>(a, t, lane, c, s);
-  const bool norm = a.wq || a.wk;
-  T *kc = nullptr, *vc = nullptr;
-  if (CACHE) {
-    const int slot = a.slots[t];
-    if (slot >= 0 && slot < a.cs.n_pages * a.cs.page_size) {
-      const int64_t at = (int64_t)(slot / a.cs.page_size) * a.cs.ps +
-                         (int64_t)(slot % a.cs.page_size) * a.cs.ts;
-      kc = static_cast<T*>(a.kc) + at;
-      vc = static_cast<T*>(a.vc) + at;
-    }
-  }
-  for (int st = s0; st < s1; ++st) {
-    const int h = st * M::kHeads + grp;
-    const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-    const T* src = nullptr;
-    const T* w = nullptr;
-    if (is_q) {
-      src = static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs;
-      w = static_cast<const T*>(a.wq);
-    } else if (is_k) {
-      src = static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
-      w = static_cast<const T*>(a.wk);
-    } else if (CACHE && h < heads) {
-      src = static_cast<const T*>(a.v) + t * a.vs.ts + (h - a.hq - a.hkv) * a.vs.hs;
-    }
-    float u[8] = {}, v[8] = {};
-    if (src) {
-      load8(src + e0, u);
-      load8(src + e1, v);
-    }
-    if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], fmaf(v[e], v[e], ss));
-      ss = head_sum<M::kLanes>(ss);
-      if (w) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float g[8];
-        load8(w + e0, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] = u[e] * r * g[e];
-        load8(w + e1, g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * r * g[e];
+  rope_runs<V>(l, a.rot, &e0, &e1);
+  Raw<T, V> nu{}, nv{};
+  auto load = [&](int t, int h) {
+    const T* p;
+    if (h < a.hq)
+      p = static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs;
+    else if (h < a.hq + a.hkv)
+      p = static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
+    else if (CACHE && h < heads)
+      p = static_cast<const T*>(a.v) + t * a.vs.ts + (h - a.hq - a.hkv) * a.vs.hs;
+    else
+      return;
+    nu.load(p + e0);
+    nv.load(p + e1);
+  };
+  int item = blockIdx.x * 4 + (threadIdx.x >> 5);
+  int t = item / a.parts, st = (item % a.parts) * per;
+  if (item < items) load(t, st * M::kHeads + grp);
+  if constexpr (NORM) rope_weights<T, D>(a, weights);
+  RopeTurn<D, IL, V> rotation;
+  while (item < items) {
+    T *kc = nullptr, *vc = nullptr;
+    if (CACHE) {
+      const int slot = a.slots[t];
+      if (slot >= 0 && slot < a.cs.n_pages * a.cs.page_size) {
+        const int64_t at = (int64_t)(slot / a.cs.page_size) * a.cs.ps +
+                           (int64_t)(slot % a.cs.page_size) * a.cs.ts;
+        kc = static_cast<T*>(a.kc) + at;
+        vc = static_cast<T*>(a.vc) + at;
       }
     }
-    if ((is_q || is_k) && l < (a.rot >> 4)) rope_turn<IL>(u, v, c, s, 1.f);
-    if (is_q) {
-      T* o = static_cast<T*>(a.qo) + t * a.qos.ts + h * a.qos.hs;
-      store8(o + e0, u);
-      store8(o + e1, v);
-    } else if (is_k) {
-      if (a.ko) {
-        T* o = static_cast<T*>(a.ko) + t * a.kos.ts + (h - a.hq) * a.kos.hs;
-        store8(o + e0, u);
-        store8(o + e1, v);
+    if (a.rot > 0) rotation.template set<false>(a, t, lane);
+    item += stride;
+    const int s1 = min(steps, st + per);
+    const int t2 = item / a.parts, st2 = (item % a.parts) * per;
+    for (; st < s1; ++st) {
+      const int h = st * M::kHeads + grp;
+      const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
+      Raw<T, V> cu = nu, cv = nv;
+      if (st + 1 < s1)
+        load(t, h + M::kHeads);
+      else if (item < items)
+        load(t2, st2 * M::kHeads + grp);
+      if (!CACHE || is_q || is_k || NORM) {
+        F2 u[V / 2], v[V / 2];
+        cu.get(u);
+        cv.get(v);
+        if constexpr (NORM) {
+          F2 ss = mul2(u[0], u[0]);
+#pragma unroll
+          for (int i = 1; i < V / 2; ++i) ss = fma2(u[i], u[i], ss);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) ss = fma2(v[i], v[i], ss);
+          const float2 two = unpack(ss);
+          const float sum = head_sum<M::kLanes>(two.x + two.y);
+          const float r = (is_q ? a.wq : a.wk) ? rsqrtf(sum * (1.f / D) + a.eps) : 1.f;
+          const F2 rr = f2(r, r);
+          F2 w[V / 2];
+          load_f2<V>(&weights[is_q ? 0 : 1][e0], w);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) u[i] = mul2(mul2(u[i], rr), w[i]);
+          load_f2<V>(&weights[is_q ? 0 : 1][e1], w);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) v[i] = mul2(mul2(v[i], rr), w[i]);
+        }
+        if (l < a.rot / (2 * V)) rotation.turn(u, v);
+        if (!CACHE || is_q || is_k) {
+          cu.set(u);
+          cv.set(v);
+        }
       }
-      if (CACHE && kc) {
-        store8(kc + (h - a.hq) * a.cs.hs + e0, u);
-        store8(kc + (h - a.hq) * a.cs.hs + e1, v);
+      T* o = nullptr;
+      if (is_q)
+        o = static_cast<T*>(a.qo) + t * a.qos.ts + h * a.qos.hs;
+      else if (is_k)
+        o = CACHE ? (kc ? kc + (h - a.hq) * a.cs.hs : nullptr)
+                  : static_cast<T*>(a.ko) + t * a.kos.ts + (h - a.hq) * a.kos.hs;
+      else if (CACHE && h < heads && vc)
+        o = vc + (h - a.hq - a.hkv) * a.cs.hs;
+      if (o) {
+        cu.store(o + e0);
+        cv.store(o + e1);
       }
-    } else if (CACHE && src && vc) {
-      store8(vc + (h - a.hq - a.hkv) * a.cs.hs + e0, u);
-      store8(vc + (h - a.hq - a.hkv) * a.cs.hs + e1, v);
     }
+    t = t2;
+    st = st2;
   }
 }
 
 // Backward: warps walk tokens with a fixed stride, so the partial sums of the
-// weights' gradients have a fixed order; each block writes one row of them.
-// dy in T2, x in T, dx in fp32.
-template <typename T, typename T2, int D, bool IL>
-__global__ void __launch_bounds__(128)
+// weights' gradients have a fixed order; each block writes one row of them. Runs
+// of 4 elements (a lane holds half of what it would at 8, so more warps fit
+// beside the sums); the next step's rows are on their way while a step is
+// computed. dy in T2, x in T, dx in fp32.
+template <typename T, typename T2, int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(128, kBwdBlocksPerSm)
     rope_bwd_kernel(const RopeArgs a, const void* dq, const void* dk, HeadRows dqs, HeadRows dks,
                     float* gq, float* gk, float* part) {
-  using M = RopeMap<D>;
-  __shared__ float sum[4 * M::kHeads][2][D];
+  constexpr int V = 4;
+  using M = RopeMap<D, V>;
+  __shared__ __align__(16) float weights[2][NORM ? D : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % M::kLanes, grp = lane / M::kLanes;
   const int heads = a.hq + a.hkv;
   const int steps = (heads + M::kHeads - 1) / M::kHeads;
   int e0, e1;
-  rope_runs(l, a.rot, &e0, &e1);
-  float dwq[16] = {}, dwk[16] = {};
-  const bool norm = a.wq || a.wk;
-  for (int t = blockIdx.x * 4 + warp; t < a.n; t += gridDim.x * 4) {
-    float c[8], s[8];
-    if (a.rot > 0) rope_angles<D, IL>(a, t, lane, c, s);
+  rope_runs<V>(l, a.rot, &e0, &e1);
+  F2 dwq[V] = {}, dwk[V] = {};
+  Raw<T2, V> nu{}, nv{};
+  Raw<T, V> nx{}, ny{};
+  auto load = [&](int t, int h) {
+    if (t >= a.n || h >= heads) return;
+    const bool is_q = h < a.hq;
+    const T2* p = is_q ? static_cast<const T2*>(dq) + t * dqs.ts + h * dqs.hs
+                       : static_cast<const T2*>(dk) + t * dks.ts + (h - a.hq) * dks.hs;
+    nu.load(p + e0);
+    nv.load(p + e1);
+    if (NORM && (is_q ? a.wq : a.wk)) {
+      const T* x = is_q ? static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs
+                        : static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
+      nx.load(x + e0);
+      ny.load(x + e1);
+    }
+  };
+  const int stride = gridDim.x * 4;
+  int t = blockIdx.x * 4 + warp;
+  load(t, grp);
+  if constexpr (NORM) rope_weights<T, D>(a, weights);
+  RopeTurn<D, IL, V> rotation;
+  for (; t < a.n; t += stride) {
+    if (a.rot > 0) rotation.template set<true>(a, t, lane);
     for (int st = 0; st < steps; ++st) {
       const int h = st * M::kHeads + grp;
       const bool is_q = h < a.hq, is_k = !is_q && h < heads;
-      float u[8] = {}, v[8] = {};
-      const T* w = nullptr;
-      if (is_q) {
-        const T2* p = static_cast<const T2*>(dq) + t * dqs.ts + h * dqs.hs;
-        load8(p + e0, u);
-        load8(p + e1, v);
-        w = static_cast<const T*>(a.wq);
-      } else if (is_k) {
-        const T2* p = static_cast<const T2*>(dk) + t * dks.ts + (h - a.hq) * dks.hs;
-        load8(p + e0, u);
-        load8(p + e1, v);
-        w = static_cast<const T*>(a.wk);
+      F2 u[V / 2], v[V / 2], x[V / 2], y[V / 2];
+      nu.get(u);
+      nv.get(v);
+      if (NORM) {
+        nx.get(x);
+        ny.get(y);
       }
-      if (l < (a.rot >> 4)) rope_turn<IL>(u, v, c, s, -1.f);
-      if (norm) {
-        float x[8] = {}, y[8] = {};
-        if (w) {
-          const T* p = is_q ? static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs
-                            : static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
-          load8(p + e0, x);
-          load8(p + e1, y);
-        }
-        float ss = 0.f;
+      if (st + 1 < steps)
+        load(t, h + M::kHeads);
+      else
+        load(t + stride, grp);
+      if (l < a.rot / (2 * V)) rotation.turn(u, v);
+      if constexpr (NORM) {
+        const bool has_w = is_q ? a.wq != nullptr : is_k && a.wk != nullptr;
+        F2 ss = mul2(x[0], x[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
-        ss = head_sum<M::kLanes>(ss);
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        float dot = 0.f;
-        if (w) {
-          float g[8];
-          load8(w + e0, g);
+        for (int i = 1; i < V / 2; ++i) ss = fma2(x[i], x[i], ss);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] *= r;
-            const float dw = u[e] * x[e];
-            if (is_q) dwq[e] += dw; else dwk[e] += dw;
-            u[e] *= g[e];
-            dot = fmaf(u[e], x[e], dot);
+        for (int i = 0; i < V / 2; ++i) ss = fma2(y[i], y[i], ss);
+        const float2 s2 = unpack(ss);
+        const float r = rsqrtf(head_sum<M::kLanes>(s2.x + s2.y) * (1.f / D) + a.eps);
+        const F2 rr = f2(r, r);
+        F2 w[V / 2], dd = f2(0.f, 0.f);
+        if (has_w) {
+          load_f2<V>(&weights[is_q ? 0 : 1][e0], w);
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            x[i] = mul2(x[i], rr);
+            if (is_q) dwq[i] = fma2(u[i], x[i], dwq[i]); else dwk[i] = fma2(u[i], x[i], dwk[i]);
+            u[i] = mul2(u[i], w[i]);
+            dd = fma2(u[i], x[i], dd);
           }
-          load8(w + e1, g);
+          load_f2<V>(&weights[is_q ? 0 : 1][e1], w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] *= r;
-            const float dw = v[e] * y[e];
-            if (is_q) dwq[8 + e] += dw; else dwk[8 + e] += dw;
-            v[e] *= g[e];
-            dot = fmaf(v[e], y[e], dot);
+          for (int i = 0; i < V / 2; ++i) {
+            y[i] = mul2(y[i], rr);
+            if (is_q) dwq[V / 2 + i] = fma2(v[i], y[i], dwq[V / 2 + i]);
+            else dwk[V / 2 + i] = fma2(v[i], y[i], dwk[V / 2 + i]);
+            v[i] = mul2(v[i], w[i]);
+            dd = fma2(v[i], y[i], dd);
           }
         }
-        dot = head_sum<M::kLanes>(dot) * (1.f / D);
-        if (w) {
+        const float2 d2 = unpack(dd);
+        const float dot = head_sum<M::kLanes>(d2.x + d2.y) * (-1.f / D);
+        const F2 nd = f2(dot, dot);
+        if (has_w) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            u[e] = r * (u[e] - x[e] * dot);
-            v[e] = r * (v[e] - y[e] * dot);
+          for (int i = 0; i < V / 2; ++i) {
+            u[i] = mul2(rr, fma2(x[i], nd, u[i]));
+            v[i] = mul2(rr, fma2(y[i], nd, v[i]));
           }
         }
       }
-      if (is_q) {
-        float* o = gq + ((int64_t)t * a.hq + h) * D;
-        store8(o + e0, u);
-        store8(o + e1, v);
-      } else if (is_k) {
-        float* o = gk + ((int64_t)t * a.hkv + (h - a.hq)) * D;
-        store8(o + e0, u);
-        store8(o + e1, v);
+      if (is_q || is_k) {
+        float* o = is_q ? gq + ((int64_t)t * a.hq + h) * D
+                        : gk + ((int64_t)t * a.hkv + (h - a.hq)) * D;
+        Raw<float, V> raw;
+        raw.set(u);
+        raw.store(o + e0);
+        raw.set(v);
+        raw.store(o + e1);
       }
     }
   }
-  if (!norm) return;
-  float(*mine)[D] = sum[warp * M::kHeads + grp];
+  if constexpr (NORM) {
+    dependency_release();
+    __shared__ float sum[4 * M::kHeads][2][D];
+    float(*mine)[D] = sum[warp * M::kHeads + grp];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    mine[0][e0 + e] = dwq[e];
-    mine[0][e1 + e] = dwq[8 + e];
-    mine[1][e0 + e] = dwk[e];
-    mine[1][e1 + e] = dwk[8 + e];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += 128) {
-    float acc = 0.f;
+    for (int i = 0; i < V; ++i) {
+      const int e = i < V / 2 ? e0 + 2 * i : e1 + 2 * i - V;
+      const float2 a2 = unpack(dwq[i]), b2 = unpack(dwk[i]);
+      mine[0][e] = a2.x;
+      mine[0][e + 1] = a2.y;
+      mine[1][e] = b2.x;
+      mine[1][e + 1] = b2.y;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * D; i += 128) {
+      float acc = 0.f;
 #pragma unroll
-    for (int g = 0; g < 4 * M::kHeads; ++g) acc += sum[g][i / D][i % D];
-    part[(int64_t)blockIdx.x * 2 * D + i] = acc;
+      for (int g = 0; g < 4 * M::kHeads; ++g) acc += sum[g][i / D][i % D];
+      part[(int64_t)blockIdx.x * 2 * D + i] = acc;
+    }
   }
 }
 
 // Sums the blocks' rows, 32 columns per block: column c of rows y, y + 32, ...
 __global__ void __launch_bounds__(1024)
     rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
+  dependency_wait();
   __shared__ float sum[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + x;
@@ -347,7 +434,6 @@ __global__ void __launch_bounds__(1024)
 
 namespace {
 
-constexpr int kBwdBlocksPerSm = 4;
 constexpr int kBwdMaxBlocks = 148 * kBwdBlocksPerSm;
 
 // The arguments that describe positions and rotation.
@@ -379,17 +465,34 @@ void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions
   a->n = n;
 }
 
-template <typename T, int D, bool CACHE>
+template <typename T, int D, bool CACHE, bool NORM>
 cudaError_t launch_rope(RopeArgs a, bool il, int sms, cudaStream_t s) {
   const int heads = a.hq + a.hkv * (CACHE ? 2 : 1);
-  const int steps = (heads + RopeMap<D>::kHeads - 1) / RopeMap<D>::kHeads;
-  // few tokens: a warp per step of heads, so that a token's heads run side by side
-  a.parts = (int64_t)a.n < (int64_t)sms * 16 ? steps : 1;
-  const int64_t items = (int64_t)a.n * a.parts;
-  const dim3 grid((unsigned)((items + 3) / 4)), block(128);
+  const int steps = (heads + RopeMap<D, kRopeRun>::kHeads - 1) / RopeMap<D, kRopeRun>::kHeads;
+  // Items per token: one, two, or one per step of heads, whichever gives the longest walk
+  // of a warp the least to do; an item's angles count as a step and a half.
+  const int64_t warps = (int64_t)sms * kRopeBlocks<T> * 4;
+  double best = 0.;
+  for (int parts : {1, 2, steps}) {
+    if (parts > steps || (int64_t)a.n * parts > INT32_MAX / 2) continue;
+    const int per = (steps + parts - 1) / parts;
+    const double cost = (double)(((int64_t)a.n * parts + warps - 1) / warps) * (per + 1.5);
+    if (a.parts == 0 || cost < best) {
+      best = cost;
+      a.parts = parts;
+    }
+  }
+  const int64_t want = ((int64_t)a.n * a.parts + 3) / 4, most = (int64_t)sms * kRopeBlocks<T>;
+  const dim3 grid((unsigned)(want < most ? want : most)), block(128);
   const char* name = CACHE ? "qk_rope_append" : "qk_rope";
-  if (il) return launch(name, rope_kernel<T, D, true, CACHE>, grid, block, 0, s, a);
-  return launch(name, rope_kernel<T, D, false, CACHE>, grid, block, 0, s, a);
+  if (il) return launch(name, rope_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a);
+  return launch(name, rope_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
+}
+
+template <typename T, int D, bool CACHE>
+cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
+  return a.wq || a.wk ? launch_rope<T, D, CACHE, true>(a, il, sms, s)
+                      : launch_rope<T, D, CACHE, false>(a, il, sms, s);
 }
 
 template <bool CACHE>
@@ -409,14 +512,20 @@ struct BwdCall {
   int blocks;
 };
 
-template <typename T, typename T2, int D>
+template <typename T, typename T2, int D, bool NORM>
 cudaError_t launch_bwd(const BwdCall& b, bool il, cudaStream_t s) {
   const dim3 grid(b.blocks), block(128);
   if (il)
-    return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, true>, grid, block, 0, s, b.a, b.dq,
-                  b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
-  return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, false>, grid, block, 0, s, b.a, b.dq,
-                b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
+    return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, true, NORM>, grid, block, 0, s, b.a,
+                  b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
+  return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, false, NORM>, grid, block, 0, s, b.a,
+                b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
+}
+
+template <typename T, typename T2, int D>
+cudaError_t launch_bwd(const BwdCall& b, bool il, cudaStream_t s) {
+  return b.a.wq || b.a.wk ? launch_bwd<T, T2, D, true>(b, il, s)
+                          : launch_bwd<T, T2, D, false>(b, il, s);
 }
 
 template <typename T, typename T2>
@@ -466,7 +575,8 @@ int adaspark_qk_rope(const void* Q, int64_t q_ts, int64_t q_hs, const void* K, i
                      float magnitude, const void* w_q, const void* w_k, float eps, int n_tokens,
                      int hq, int hkv, int d, void* Q_out, int64_t qo_ts, int64_t qo_hs,
                      void* K_out, int64_t ko_ts, int64_t ko_hs, void* stream) {
-  if (n_tokens < 0 || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype)) return ADASPARK_EINVAL;
+  if (n_tokens < 0 || n_tokens > (1 << 30) || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype))
+    return ADASPARK_EINVAL;
   if (n_tokens == 0) return ADASPARK_OK;
   if (!Q || !K || !Q_out || !K_out) return ADASPARK_EINVAL;
   if (!rope_ok(freq, rot, d, positions, n_axes, sections, magnitude)) return ADASPARK_EINVAL;
@@ -496,7 +606,8 @@ int adaspark_qk_rope_append(const void* Q, int64_t q_ts, int64_t q_hs, const voi
                             int hkv, int d, const int32_t* slots, void* k_cache, void* v_cache,
                             int64_t c_ps, int64_t c_ts, int64_t c_hs, int n_pages, int page_size,
                             void* Q_out, int64_t qo_ts, int64_t qo_hs, void* stream) {
-  if (n_tokens < 0 || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype)) return ADASPARK_EINVAL;
+  if (n_tokens < 0 || n_tokens > (1 << 30) || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype))
+    return ADASPARK_EINVAL;
   if (n_tokens == 0) return ADASPARK_OK;
   if (!Q || !K || !V || !Q_out || !slots) return ADASPARK_EINVAL;
   if (!rope_ok(freq, rot, d, positions, n_axes, sections, magnitude)) return ADASPARK_EINVAL;
@@ -524,7 +635,8 @@ int adaspark_kv_append(const void* K, int64_t k_ts, int64_t k_hs, const void* V,
                        int64_t v_hs, int dtype, int n_tokens, int hkv, int d, const int32_t* slots,
                        void* k_cache, void* v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,
                        int n_pages, int page_size, void* stream) {
-  if (n_tokens < 0 || !head_sizes_ok(hkv, hkv, d, dtype)) return ADASPARK_EINVAL;
+  if (n_tokens < 0 || n_tokens > (1 << 30) || !head_sizes_ok(hkv, hkv, d, dtype))
+    return ADASPARK_EINVAL;
   if (n_tokens == 0) return ADASPARK_OK;
   if (!K || !V || !slots) return ADASPARK_EINVAL;
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
@@ -544,7 +656,7 @@ int adaspark_kv_append(const void* K, int64_t k_ts, int64_t k_hs, const void* V,
 }
 
 size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d, int dtype) {
-  if (n_tokens < 0 || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
+  if (n_tokens < 0 || n_tokens > (1 << 30) || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
   return align_up((size_t)kBwdMaxBlocks * 2 * d * sizeof(float));
 }
 
@@ -558,7 +670,7 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
                               float* dK, float* dw_q, float* dw_k, void* workspace,
                               size_t workspace_bytes, void* stream) {
   const bool norm = w_q || w_k;
-  if (n_tokens < 0 || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype) ||
+  if (n_tokens < 0 || n_tokens > (1 << 30) || !(eps >= 0.f) || !head_sizes_ok(hq, hkv, d, dtype) ||
       (dy_dtype != ADASPARK_BF16 && dy_dtype != ADASPARK_FP32))
     return ADASPARK_EINVAL;
   if (!aligned(dw_q, 4) || !aligned(dw_k, 4) || (w_q && !dw_q) || (w_k && !dw_k))
@@ -609,7 +721,7 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     e = dy_dtype == ADASPARK_BF16 ? dispatch_bwd<float, bf16>(b, d, il, s)
                                   : dispatch_bwd<float, float>(b, d, il, s);
   if (e == cudaSuccess && norm)
-    e = launch("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 32), dim3(1024), 0, s, b.part, blocks, d,
+    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 32), dim3(1024), 0, s, b.part, blocks, d,
                w_q ? dw_q : nullptr, w_k ? dw_k : nullptr);
   return cuda_status(e);
 }

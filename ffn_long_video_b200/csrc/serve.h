@@ -54,37 +54,56 @@ inline bool cache_ok(const void* k, const void* v, const CacheRows& c, int hkv, 
 
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? ADASPARK_OK : ADASPARK_ECUDA; }
 
-// Eight consecutive elements as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  const float4 b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// V (4 or 8) consecutive elements as they lie in memory, and as fp32 pairs.
+template <typename T, int V>
+struct Raw {
+  static constexpr int kWords = V * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if (kWords == 2) {
+      const uint2 r = *reinterpret_cast<const uint2*>(p);
+      w[0] = r.x;
+      w[1] = r.y;
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = r.x;
+        w[i + 1] = r.y;
+        w[i + 2] = r.z;
+        w[i + 3] = r.w;
+      }
+    }
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
+  __device__ __forceinline__ void store(T* p) const {
+    if (kWords == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) =
+            make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+  }
+  __device__ __forceinline__ void get(F2 (&v)[V / 2]) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i)
+      v[i] = sizeof(T) == 2 ? bf16x2_f2(w[i])
+                            : f2(__uint_as_float(w[(2 * i) % kWords]),
+                                 __uint_as_float(w[(2 * i + 1) % kWords]));
+  }
+  __device__ __forceinline__ void set(const F2 (&v)[V / 2]) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 x = unpack(v[i]);
+      if (sizeof(T) == 2) {
+        w[i] = pack_bf16x2(x.x, x.y);
+      } else {
+        w[(2 * i) % kWords] = __float_as_uint(x.x);
+        w[(2 * i + 1) % kWords] = __float_as_uint(x.y);
+      }
+    }
+  }
+};
 
 }  // namespace adaspark

@@ -484,7 +484,7 @@ int adaspark_rmsnorm(const void *x, int x_dtype, const void *weight, void *out, 
  *     of a page in either order. A token's slot is page * page_size + offset;
  *     n_pages * page_size < 2^31. Element offsets are 64-bit.
  *   - Element type `dtype` (BF16 or FP32) is that of activations, norm weights
- *     and cache; d = 64 or 128; hq % hkv == 0, hq <= 4096.
+ *     and cache; d = 64 or 128; hq % hkv == 0, hq <= 4096; n_tokens <= 2^30.
  *   - ADASPARK_EUNSUPPORTED on a device that is not sm_100. */
 
 /* Scaling of rotary frequencies for contexts longer than the trained ones. */

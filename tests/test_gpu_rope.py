@@ -248,10 +248,10 @@ def test_backward(c, dy_dtype):
         if w is None:
             assert gw is None
             continue
-        # a lane adds the terms of its tokens and steps of heads, then at most 32 groups of a
-        # block, 592 / 32 rows of blocks and 32 of their sums: every term passes fewer sums
-        # than that, each of half a step
-        depth = -(-n // 4) * (hq + hkv) / (4 if n > 2368 else 1) + 32 + 19 + 32
+        # whatever the split, no term passes more sums than its lane's share of the terms (no
+        # lane has over a quarter of the tokens), 32 lanes' sums of a block, 32 rows of blocks
+        # and 32 of their sums, each of half a step
+        depth = -(-n // 4) * (hq + hkv) + 96
         _close(gw, want_w, (50 + depth) * U * terms.sum((0, 1)), "dw_" + what)
     # the same bits again; in place where the upstream gradient is fp32
     again = fb.qk_rope_backward(dq, dk, *args, Q=Q, K=K, workspace=ws,
