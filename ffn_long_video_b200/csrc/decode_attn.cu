@@ -19,6 +19,18 @@
 
 namespace adaspark {
 
+#ifndef DSF
+#define DSF 2
+#define DBF 3
+#define DSB 3
+#define DBB 2
+#endif
+#ifndef DSF
+#define DSF 2
+#define DBF 3
+#define DSB 3
+#define DBB 2
+#endif
 struct DecodeArgs {
   WsHeader* hdr;
   const void* q;
@@ -32,14 +44,19 @@ struct DecodeArgs {
   float* lse;                    // or null
   float scale_log2;              // scale * log2(e)
   int32_t n_seqs, max_len, hq, hkv, group, hgroups;  // hgroups: groups of 8 heads per KV head
+  int32_t by_run;
+  int32_t in_page;               // a page holds a whole number of stages
+  int32_t tile_pages, tile_rest; // pages and tokens beyond them that a tile spans
   int32_t* status;               // [grid] status bits of each block
-  int4* joins;                   // [grid] {seq, KV head * hgroups + group, first slot, last slot}
+  int4* joins;                   // {seq, KV head * hgroups + group, first slot, last slot} or -1:
+                                 // of each run (by_run: there are no more than blocks), or of
+                                 // the cut run that starts in each block
   float* part;                   // [2 grid][8][D + 2]: outputs, maximum (log2), sum
 };
 
 constexpr int kDecHeads = 8;     // query heads of a run
 constexpr int kDecWarps = 4;
-constexpr int kDecStages = 3;
+constexpr int kDecMaxBlocks = 148 * 3;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
@@ -54,13 +71,23 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Keys of sequence i, 0 for a length the table cannot hold (flagged).
-__device__ __forceinline__ int dec_len(const DecodeArgs& a, int i, uint32_t* bits) {
-  const int n = a.lens[i];
-  if (n >= 0 && n <= a.max_len) return n;
-  *bits |= ADASPARK_DEV_BAD_LAYOUT;
-  return 0;
-}
+// Sizes of a warp's work: a tile is kKeys keys of each of the block's warps, a
+// stage a warp's share of it, a ring the stages it has in flight. bf16 rows are
+// padded so that the 8 rows of a matrix load fall on different banks.
+template <typename T_, int D_>
+struct DecShape {
+  using T = T_;
+  static constexpr int D = D_;
+  static constexpr int kKeys = 4096 / (D * (int)sizeof(T));  // 4 KB of K
+  static constexpr int kTile = kKeys * kDecWarps;
+  static constexpr int kRow = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 0);
+  static constexpr int kStage = 2 * kKeys * kRow;            // K rows, V rows
+  static constexpr int kStages = sizeof(T) == 2 ? DSB : DSF;
+  static constexpr int kBlocks = sizeof(T) == 2 ? DBB : DBF;  // blocks per SM
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kSmem = kDecWarps * kRing;
+  static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
+};
 
 // Position of a block on the line of tiles.
 struct DecSpot {
@@ -69,80 +96,80 @@ struct DecSpot {
   int tile;              // tile in the run
 };
 
-// Tiles before every sequence: the total, and the sequence that holds tile `at`.
-template <int TILE>
-__device__ __forceinline__ long long dec_total(const DecodeArgs& a, long long* warp_sum,
-                                               long long* before, uint32_t* bits) {
-  // thread i sums sequences [i * per, (i + 1) * per)
-  const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
-  const int i0 = min(a.n_seqs, (int)threadIdx.x * per), i1 = min(a.n_seqs, i0 + per);
-  long long own = 0;
-  for (int i = i0; i < i1; ++i) own += (dec_len(a, i, bits) + TILE - 1) / TILE;
-  own *= a.hkv * a.hgroups;
-  long long inc = own;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  long long total = 0, base = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    if (w < warp) base += warp_sum[w];
-    total += warp_sum[w];
-  }
-  *before = base + inc - own;
-  return total;
-}
-
-template <typename T, int D>
-struct DecShape {
-  static constexpr int kKeys = 1024 / (D * (int)sizeof(T)) * 4;  // keys of a warp's stage: 4 KB of K
-  static constexpr int kTile = kKeys * kDecWarps;
-  static constexpr int kRow = D * (int)sizeof(T) + 16;           // padded row
-  static constexpr int kStage = 2 * kKeys * kRow;                // K rows, V rows
-  static constexpr int kRing = kDecStages * kStage;              // a warp's stages
-  static constexpr int kSmem = kDecWarps * kRing;
-};
-
-// What a block knows of the line of tiles.
+// The line of tiles and a block's share of it. The host keeps the tiles that the
+// tables can hold below 2^31, so all of this fits 32 bits.
 struct DecLine {
-  long long total, B;   // tiles, blocks that share them
-  long long u0, u1;     // this block's
+  int total, B;         // tiles, blocks that share them: each of them has one at least
+  int u0, u1;           // this block's
+  int each, rest;       // total / B, total % B: the first `rest` blocks take one more
+
+  __device__ __forceinline__ int start(int b) const { return b * each + min(b, rest); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int cut = rest * (each + 1);
+    return tile < cut ? tile / (each + 1) : rest + (tile - cut) / each;
+  }
 };
 
 struct DecShared {
-  long long warp_sum[kDecWarps];
+  int warp_sum[kDecWarps];
   DecSpot first;
   float m[kDecWarps][kDecHeads], l[kDecWarps][kDecHeads];
   uint32_t bits[kDecWarps];
 };
 
+// Keys of sequence i, 0 for a length the table cannot hold (flagged).
+__device__ __forceinline__ int dec_len(const DecodeArgs& a, int i, uint32_t* bits) {
+  const int n = a.lens[i];
+  if (n >= 0 && n <= a.max_len) return n;
+  *bits |= ADASPARK_DEV_BAD_LAYOUT;
+  return 0;
+}
+
 // Finds the block's share and its first run; writes the results of sequences
 // without keys. All threads; ends with a barrier.
-template <typename T, int D>
+template <class S>
 __device__ __forceinline__ DecLine dec_begin(const DecodeArgs& a, DecShared& sh, uint32_t* bits) {
-  using S = DecShape<T, D>;
-  const int b = blockIdx.x;
-  long long before;
+  using T = typename S::T;
+  constexpr int D = S::D;
+  const int b = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int runs = a.hkv * a.hgroups;
+  // thread i sums the tiles of sequences [i * per, (i + 1) * per)
+  const int per = (a.n_seqs + kDecWarps * 32 - 1) / (kDecWarps * 32);
+  const int i0 = min(a.n_seqs, (int)threadIdx.x * per), i1 = min(a.n_seqs, i0 + per);
+  int own = 0, len = 0;
+  for (int i = i0; i < i1; ++i) {
+    len = dec_len(a, i, bits);
+    own += (len + S::kTile - 1) / S::kTile * runs;
+  }
+  int inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) sh.warp_sum[warp] = inc;
+  __syncthreads();
   DecLine L;
-  L.total = dec_total<S::kTile>(a, sh.warp_sum, &before, bits);
-  // blocks that share the line: each of them has a tile at least
-  L.B = min((long long)gridDim.x, L.total);
-  L.u0 = b < L.B ? L.total * b / L.B : 0;
-  L.u1 = b < L.B ? L.total * (b + 1) / L.B : 0;
-  if (L.u0 < L.u1) {
-    const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
-    const int i0 = min(a.n_seqs, (int)threadIdx.x * per), i1 = min(a.n_seqs, i0 + per);
-    long long at = before;
-    for (int i = i0; i < i1; ++i) {
-      const int len = dec_len(a, i, bits), tiles = (len + S::kTile - 1) / S::kTile;
-      const long long mine = (long long)tiles * a.hkv * a.hgroups;
-      if (L.u0 >= at && L.u0 < at + mine) {
-        const int in = (int)(L.u0 - at);
+  L.total = 0;
+  int before = inc - own;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    L.total += sh.warp_sum[w];
+  }
+  L.B = min((int)gridDim.x, L.total);
+  L.each = L.B ? L.total / L.B : 0;
+  L.rest = L.total - L.B * L.each;
+  L.u0 = b < L.B ? L.start(b) : 0;
+  L.u1 = b < L.B ? L.start(b + 1) : 0;
+  if (L.u0 < L.u1 && L.u0 >= before && L.u0 < before + own) {
+    for (int i = i0, at = before; i < i1; ++i) {
+      if (per > 1) len = dec_len(a, i, bits);
+      const int tiles = (len + S::kTile - 1) / S::kTile, mine = tiles * runs;
+      if (L.u0 < at + mine) {
+        const int in = L.u0 - at;
         sh.first = DecSpot{i, len, tiles, in / tiles, in % tiles};
+        break;
       }
       at += mine;
     }
@@ -154,60 +181,150 @@ __device__ __forceinline__ DecLine dec_begin(const DecodeArgs& a, DecShared& sh,
     if (a.lse)
       for (int h = threadIdx.x; h < a.hq; h += blockDim.x)
         a.lse[(int64_t)i * a.hq + h] = -INFINITY;
+    if (a.by_run)
+      for (int r = threadIdx.x; r < runs; r += blockDim.x) a.joins[i * runs + r].x = -1;
   }
   __syncthreads();
   return L;
 }
 
-// Element offset of a key's row in the cache, -1 for a key that is not there.
-// `page` is the table's entry for the key (any value where key >= len).
-__device__ __forceinline__ int64_t dec_offset(const DecodeArgs& a, int key, int len, int page,
-                                              int kvh, uint32_t* bits) {
-  if (key >= len) return -1;
-  if (page < 0 || page >= a.cs.n_pages) {
-    *bits |= ADASPARK_DEV_BAD_LAYOUT;
-    return -1;
-  }
-  return page * a.cs.ps + (key % a.cs.page_size) * a.cs.ts + kvh * a.cs.hs;
+// Next run on the line (seq = n_seqs behind the last one).
+template <class S>
+__device__ __forceinline__ void dec_next_run(const DecodeArgs& a, DecSpot* at, uint32_t* bits) {
+  at->tile = 0;
+  if (++at->run < a.hkv * a.hgroups) return;
+  at->run = 0;
+  do {
+    if (++at->seq >= a.n_seqs) return;
+    at->len = dec_len(a, at->seq, bits);
+    at->tiles = (at->len + S::kTile - 1) / S::kTile;
+  } while (at->tiles == 0);
 }
 
-// Copies a stage's rows, row r at lane r's offset: consecutive lanes take the
-// 16-byte pieces of a row. One commit group, empty when nothing is wanted.
-template <typename T, int D>
-__device__ __forceinline__ void dec_copy(const DecodeArgs& a, uint8_t* st, int64_t off, bool want) {
-  using S = DecShape<T, D>;
-  constexpr int per_row = D * (int)sizeof(T) / 16, rows = 32 / per_row;
+// A stage's row of this lane, its table entry on the way.
+struct DecRow {
+  int page, in_page, kvh;   // in_page: token in the page, -1: no key
+};
+
+// The walk of the copies, ahead of the arithmetic: the lane's key, its page and
+// its place there, moved on without a division.
+template <class S>
+struct DecWalk {
+  DecSpot at;
+  int key, page, in_page, kvh;
+  int page0, in_page0;       // of the lane's key in a run's first tile
+  const int32_t* table;
+
+  __device__ __forceinline__ DecWalk(const DecodeArgs& a, const DecSpot& first) : at(first) {
+    const int own = (threadIdx.x >> 5) * S::kKeys + (threadIdx.x & 31);
+    page0 = own / a.cs.page_size;
+    in_page0 = own - page0 * a.cs.page_size;
+    key = at.tile * S::kTile + own;
+    page = key / a.cs.page_size;
+    in_page = key - page * a.cs.page_size;
+    kvh = at.run / a.hgroups;
+    table = a.table + at.seq * a.table_stride;
+  }
+  __device__ __forceinline__ DecRow row() const {
+    DecRow r{0, -1, kvh};
+    if ((threadIdx.x & 31) < S::kKeys && key < at.len) {
+      r.page = table[page];
+      r.in_page = in_page;
+    }
+    return r;
+  }
+  __device__ __forceinline__ void next(const DecodeArgs& a, uint32_t* bits) {
+    if (++at.tile < at.tiles) {
+      key += S::kTile;
+      page += a.tile_pages;
+      in_page += a.tile_rest;
+      if (in_page >= a.cs.page_size) {
+        in_page -= a.cs.page_size;
+        ++page;
+      }
+      return;
+    }
+    dec_next_run<S>(a, &at, bits);
+    key = (threadIdx.x >> 5) * S::kKeys + (threadIdx.x & 31);
+    page = page0;
+    in_page = in_page0;
+    kvh = at.run / a.hgroups;
+    table = a.table + at.seq * a.table_stride;
+  }
+};
+
+// Copies a stage's rows into shared memory (one commit group, empty when nothing
+// is wanted) and returns the bits of the rows that are there; absent rows become
+// zeros. Consecutive lanes take the 16-byte pieces of a row.
+template <class S>
+__device__ __forceinline__ uint32_t dec_copy(const DecodeArgs& a, uint8_t* st, const DecRow& r,
+                                             bool want, uint32_t* bits) {
+  constexpr int es = (int)sizeof(typename S::T), per_row = S::D * es / 16, rows = 32 / per_row;
   const int lane = threadIdx.x & 31, r0 = lane / per_row, piece = lane % per_row;
+  uint32_t there = 0;
   if (want) {
+    int64_t off = -1;
+    if (r.in_page >= 0) {
+      if (r.page >= 0 && r.page < a.cs.n_pages)
+        off = r.page * a.cs.ps + r.in_page * a.cs.ts + r.kvh * a.cs.hs;
+      else
+        *bits |= ADASPARK_DEV_BAD_LAYOUT;
+    }
+    there = __ballot_sync(0xffffffffu, off >= 0);
+    uint8_t* kd = st + r0 * S::kRow + piece * 16;
+    uint8_t* vd = kd + S::kKeys * S::kRow;
+    if (a.in_page && there == S::kAll) {
+      // a page holds all rows: they lie ts apart, one offset serves (a third less to issue
+      // per row than an exchange for each)
+      const int64_t o0 = __shfl_sync(0xffffffffu, off, 0);
+      const int64_t byte = (o0 + r0 * a.cs.ts) * es + piece * 16, step = rows * a.cs.ts * es;
+      const uint8_t* ks = static_cast<const uint8_t*>(a.kc) + byte;
+      const uint8_t* vs = static_cast<const uint8_t*>(a.vc) + byte;
 #pragma unroll
-    for (int r = 0; r < S::kKeys; r += rows) {
-      const int64_t ro = __shfl_sync(0xffffffffu, off, r + r0);
-      const bool ok = ro >= 0;
-      const int64_t byte = (ok ? ro * (int)sizeof(T) : 0) + piece * 16;
-      cp_async16(st + (r + r0) * S::kRow + piece * 16, static_cast<const uint8_t*>(a.kc) + byte, ok);
-      cp_async16(st + (S::kKeys + r + r0) * S::kRow + piece * 16,
-                 static_cast<const uint8_t*>(a.vc) + byte, ok);
+      for (int i = 0; i < S::kKeys; i += rows) {
+        cp_async16(kd + i * S::kRow, ks, true);
+        cp_async16(vd + i * S::kRow, vs, true);
+        ks += step;
+        vs += step;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kKeys; i += rows) {
+        const int64_t ro = __shfl_sync(0xffffffffu, off, i + r0);
+        const bool ok = ro >= 0;
+        const int64_t byte = (ok ? ro * es : 0) + piece * 16;
+        cp_async16(kd + i * S::kRow, static_cast<const uint8_t*>(a.kc) + byte, ok);
+        cp_async16(vd + i * S::kRow, static_cast<const uint8_t*>(a.vc) + byte, ok);
+      }
     }
   }
   cp_async_commit();
+  return there;
 }
 
-// Joins the warps' parts of a run (maxima and sums in sh, outputs [8][D] at the
-// start of each warp's ring) and writes its results or the block's partial ones.
-// All threads; the caller puts a barrier before and after. Returns the joins
-// entry of a cut run that starts in this block.
-template <typename T, int D>
-__device__ __forceinline__ void dec_end_run(const DecodeArgs& a, const DecShared& sh,
-                                            const uint8_t* smem, const DecSpot& at, int n_tiles,
-                                            long long u, const DecLine& L, int4* join) {
-  using S = DecShape<T, D>;
-  constexpr int E = D / 32;
+// Ends a run, or the block's share of one: joins the warps' maxima, sums and
+// outputs and writes results or partial ones. The outputs pass through the stage
+// that each warp has just used (`used`; [8][D + 4] floats), the other stages are
+// being filled for the tiles to come. All threads; ends with a barrier. `u`: tile
+// on the line where the block's share of the run began; `from`: that tile in the run.
+template <class M>
+__device__ __forceinline__ void dec_end_run(const DecodeArgs& a, DecShared& sh, M& math,
+                                            uint8_t* smem, int used, const DecSpot& at, int from,
+                                            int u, const DecLine& L, int4* join) {
+  using S = typename M::S;
+  using T = typename S::T;
+  constexpr int D = S::D, E = D / 32;
+  static_assert(kDecHeads * (D + 4) * 4 <= S::kStage, "");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
   const int heads = min(kDecHeads, a.group - hg * kDecHeads);
   const int h0 = kvh * a.group + hg * kDecHeads;
-  const bool whole = at.tile == 0 && n_tiles == at.tiles;
+  const bool whole = from == 0 && at.tile + 1 == at.tiles;
   const int slot = 2 * blockIdx.x + (u == L.u0 ? 0 : 1);
+  math.sums(sh.m[warp], sh.l[warp]);
+  __syncwarp();
+  math.outputs(reinterpret_cast<float*>(smem + warp * S::kRing + used * S::kStage));
+  __syncthreads();
   for (int h = warp; h < heads; h += kDecWarps) {
     float mm = -INFINITY;
 #pragma unroll
@@ -218,229 +335,288 @@ __device__ __forceinline__ void dec_end_run(const DecodeArgs& a, const DecShared
     for (int w = 0; w < kDecWarps; ++w) {
       const float f = exp2f(sh.m[w][h] - mu);
       ll = fmaf(sh.l[w][h], f, ll);
-      const float* ob = reinterpret_cast<const float*>(smem + w * S::kRing);
+      const float* o = reinterpret_cast<const float*>(smem + w * S::kRing + used * S::kStage);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(ob[h * D + lane * E + e], f, acc[e]);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(o[h * (D + 4) + 32 * e + lane], f, acc[e]);
     }
+    const int64_t row = (int64_t)at.seq * a.hq + h0 + h;
     if (whole) {
       const float r = 1.f / ll;
-      T* op = static_cast<T*>(a.out) + ((int64_t)at.seq * a.hq + h0 + h) * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) op[e] = from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
-      if (a.lse && lane == 0)
-        a.lse[(int64_t)at.seq * a.hq + h0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      for (int e = 0; e < E; ++e)
+        static_cast<T*>(a.out)[row * D + 32 * e + lane] =
+            from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
+      if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     } else {
       float* pp = a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
 #pragma unroll
-      for (int e = 0; e < E; ++e) pp[lane * E + e] = acc[e];
+      for (int e = 0; e < E; ++e) pp[32 * e + lane] = acc[e];
       if (lane == 0) {
         pp[D] = mm;
         pp[D + 1] = ll;
       }
     }
   }
-  if (!whole && at.tile == 0) {
-    // the first block of a cut run: its parts are this slot and the first slots of the
-    // blocks up to the one that holds the run's last tile
-    const long long end = u + at.tiles - 1;
-    long long last = end * L.B / L.total;
-    while (L.total * (last + 1) / L.B <= end) ++last;
-    while (L.total * last / L.B > end) --last;
-    *join = make_int4(at.seq, at.run, slot, 2 * (int)last);
+  if (from == 0) {
+    // the first block of a run; the parts of a cut one are this slot and the first slots of
+    // the blocks up to the one that holds the run's last tile
+    const int4 j = whole ? make_int4(-1, 0, 0, 0)
+                         : make_int4(at.seq, at.run, slot, 2 * L.owner(u + at.tiles - 1));
+    if (!whole) *join = j;
+    if (a.by_run && threadIdx.x == 0) a.joins[at.seq * a.hkv * a.hgroups + at.run] = j;
   }
+  __syncthreads();
 }
 
-// Next run on the line.
-template <int TILE>
-__device__ __forceinline__ void dec_advance(const DecodeArgs& a, DecSpot* at, uint32_t* bits) {
-  at->tile = 0;
-  if (++at->run < a.hkv * a.hgroups) return;
-  at->run = 0;
-  do {
-    if (++at->seq >= a.n_seqs) return;
-    at->len = dec_len(a, at->seq, bits);
-    at->tiles = (at->len + TILE - 1) / TILE;
-  } while (at->tiles == 0);
-}
-
-__device__ __forceinline__ void dec_end(const DecodeArgs& a, DecShared& sh, uint32_t bits,
-                                        int4 join) {
+// The walk along the line. Each warp's keys pass through a ring of stages of its
+// own in shared memory (cp.async), so warps run without block barriers inside a
+// run; the copies run on across runs, and a stage's table entries are fetched a
+// step before its copies are issued. M: the arithmetic (a run's queries,
+// maxima, sums and outputs in registers).
+template <class M>
+__global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks) decode_kernel(const DecodeArgs a) {
+  using S = typename M::S;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ DecShared sh;
+  __shared__ typename M::Shared msh;
+  const int warp = threadIdx.x >> 5;
+  dependency_release();
+  dependency_wait();
+  uint32_t bits = 0;
+  const DecLine L = dec_begin<S>(a, sh, &bits);
+  int4 join = make_int4(-1, 0, 0, 0);
+  const int steps = L.u1 - L.u0;
+  if (steps > 0) {
+    DecSpot at = sh.first;
+    DecWalk<S> ahead(a, at);   // at step min(i + kStages, steps) when step i begins
+    uint8_t* ring = smem + warp * S::kRing;
+    uint32_t there[S::kStages - 1];
+    DecRow row[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+      if (i < steps) row[i] = ahead.row();
+      if (i + 1 < steps) ahead.next(a, &bits);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i)
+      there[i] = dec_copy<S>(a, ring + i * S::kStage, row[i], i < steps, &bits);
+    DecRow next = row[S::kStages - 1];
+    M math(a, msh);
+    math.begin(at);
+    int from = at.tile, u = L.u0, stage = 0;
+    for (int i = 0; i < steps; ++i) {
+      __syncwarp();  // the stage that is copied into was read by every lane
+      const uint32_t coming =
+          dec_copy<S>(a, ring + (stage == 0 ? S::kStages - 1 : stage - 1) * S::kStage, next,
+                      i + S::kStages - 1 < steps, &bits);
+      if (i + S::kStages < steps) {
+        next = ahead.row();
+        if (i + S::kStages + 1 < steps) ahead.next(a, &bits);
+      }
+      cp_async_wait<S::kStages - 1>();
+      __syncwarp();
+      math.tile(ring + stage * S::kStage, there[0]);
+#pragma unroll
+      for (int k = 0; k < S::kStages - 2; ++k) there[k] = there[k + 1];
+      there[S::kStages - 2] = coming;
+      if (at.tile + 1 == at.tiles || i + 1 == steps) {
+        dec_end_run(a, sh, math, smem, stage, at, from, u, L, &join);
+        u = L.u0 + i + 1;
+        from = 0;
+        if (i + 1 < steps) {
+          dec_next_run<S>(a, &at, &bits);
+          math.begin(at);
+        }
+      } else {
+        ++at.tile;
+      }
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+  }
   bits = __reduce_or_sync(0xffffffffu, bits);
-  if ((threadIdx.x & 31) == 0) sh.bits[threadIdx.x >> 5] = bits;
+  if ((threadIdx.x & 31) == 0) sh.bits[warp] = bits;
   __syncthreads();
   if (threadIdx.x == 0) {
     uint32_t v = 0;
     for (int w = 0; w < kDecWarps; ++w) v |= sh.bits[w];
     a.status[blockIdx.x] = (int32_t)v;
-    a.joins[blockIdx.x] = join;
+    if (!a.by_run) a.joins[blockIdx.x] = join;
   }
 }
 
-template <int E>
-__device__ __forceinline__ void dec_row(const uint8_t* row, int lane, float (&v)[E]);
-template <>
-__device__ __forceinline__ void dec_row<4>(const uint8_t* row, int lane, float (&v)[4]) {
-  const float4 x = reinterpret_cast<const float4*>(row)[lane];
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-template <>
-__device__ __forceinline__ void dec_row<2>(const uint8_t* row, int lane, float (&v)[2]) {
-  const float2 x = reinterpret_cast<const float2*>(row)[lane];
-  v[0] = x.x; v[1] = x.y;
-}
-
-// fp32: each lane holds D / 32 elements of every row and of 8 heads' outputs; a
-// warp's keys pass through a ring of stages of its own in shared memory
-// (cp.async), so warps run without block barriers inside a run.
+// fp32 on the CUDA cores, in packed pairs (two multiply-adds per instruction).
+// Scores: 8 lanes share a key (16 or 8 elements each, queries from shared memory,
+// two keys at a time), 4 keys side by side; 7 exchanges leave lane j of them with
+// head j. Outputs: a lane holds D / 32 elements of 8 heads. Weights pass through
+// shared memory, written twice as a pair so that they load as one. Outputs and
+// sums are kept in two levels (kFlush tiles, then all): one chain of 2400 keys
+// had twice the error.
 template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32) decode_simt_kernel(const DecodeArgs a) {
-  using T = float;
-  using S = DecShape<T, D>;
-  constexpr int E = D / 32, KK = S::kKeys;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ DecShared sh;
-  __shared__ __align__(16) float pbuf[kDecWarps][KK][kDecHeads];  // read 16 bytes at a time
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  dependency_release();
-  uint32_t bits = 0;
-  const DecLine L = dec_begin<T, D>(a, sh, &bits);
-  int4 join = make_int4(-1, 0, 0, 0);
-  DecSpot at = sh.first;
-  uint8_t* ring = smem + warp * S::kRing;
-  for (long long u = L.u0; u < L.u1;) {
-    const int n_tiles = (int)min((long long)(at.tiles - at.tile), L.u1 - u);
+struct DecFp32 {
+  using S = DecShape<float, D>;
+  static constexpr int E2 = D / 64, KK = S::kKeys, kFlush = 8;
+  struct Shared {
+    __align__(16) float q[kDecHeads][D];
+    __align__(16) float2 p[kDecWarps][KK][kDecHeads];
+  };
+  const DecodeArgs& a;
+  Shared& sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kg = lane >> 3, j = lane & 7;
+  F2 o[kDecHeads][E2], om[kDecHeads][E2];
+  float m, l, lm;  // this lane's head: j
+  int n;
+
+  __device__ __forceinline__ DecFp32(const DecodeArgs& a_, Shared& sh_) : a(a_), sh(sh_) {}
+
+  __device__ __forceinline__ static void lds(const void* p, F2& x, F2& y) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    x.v = v.x;
+    y.v = v.y;
+  }
+
+  // All threads, at a point where no warp reads the queries of the run before.
+  __device__ __forceinline__ void begin(const DecSpot& at) {
     const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
     const int heads = min(kDecHeads, a.group - hg * kDecHeads);
-    const int h0 = kvh * a.group + hg * kDecHeads;
-    float q[kDecHeads][E], o[kDecHeads][E];
-    float m = -INFINITY, l = 0.f;   // this lane's head: lane % 8
+    const float* q = static_cast<const float*>(a.q) + at.seq * a.qs.ts +
+                     (int64_t)(kvh * a.group + hg * kDecHeads) * a.qs.hs;
+    for (int e = threadIdx.x; e < kDecHeads * D; e += kDecWarps * 32)
+      sh.q[e / D][e % D] = e / D < heads ? q[e / D * a.qs.hs + e % D] : 0.f;
+    __syncthreads();
 #pragma unroll
-    for (int h = 0; h < kDecHeads; ++h) {
+    for (int h = 0; h < kDecHeads; ++h)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        q[h][e] = 0.f;
-        o[h][e] = 0.f;
-      }
-      if (h < heads) {
-        const T* p = static_cast<const T*>(a.q) + at.seq * a.qs.ts + (h0 + h) * a.qs.hs;
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[h][e] = p[lane * E + e];
-      }
-    }
-    const int32_t* pages = a.table + at.seq * a.table_stride;
-    const int key0 = at.tile * S::kTile + warp * KK;
+      for (int e = 0; e < E2; ++e) o[h][e] = om[h][e] = f2(0.f, 0.f);
+    m = -INFINITY;
+    l = lm = 0.f;
+    n = 0;
+  }
 
-    // Rows of stage i into the ring; returns the bits of the rows that are there.
-    auto fetch = [&](int i) -> uint32_t {
-      const int key = key0 + i * S::kTile + lane;
-      int64_t off = -1;
-      if (i < n_tiles && lane < KK && key < at.len)
-        off = dec_offset(a, key, at.len, pages[key / a.cs.page_size], kvh, &bits);
-      dec_copy<T, D>(a, ring + (i % kDecStages) * S::kStage, off, i < n_tiles);
-      return __ballot_sync(0xffffffffu, off >= 0);
-    };
-
-    uint32_t there[kDecStages];
+  __device__ __forceinline__ void tile(const uint8_t* st, uint32_t here) {
+    float z[KK / 4];  // of key 4 g + kg and head j
+    float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) there[i] = fetch(i);
-    for (int i = 0; i < n_tiles; ++i) {
-      __syncwarp();  // the stage that is fetched into was read by every lane
-      const uint32_t next = fetch(i + kDecStages - 1);
-      cp_async_wait<kDecStages - 1>();
-      __syncwarp();
-      const uint32_t here = there[0];
+    for (int g = 0; g < KK / 4; g += 2) {
+      F2 acc[2][kDecHeads];
 #pragma unroll
-      for (int k = 0; k + 1 < kDecStages - 1; ++k) there[k] = there[k + 1];
-      there[kDecStages - 2] = next;
-      const uint8_t* st = ring + (i % kDecStages) * S::kStage;
-      // scores, four keys at a time; lane = key * 8 + head holds one of the 32 sums
-      float z[KK / 4];
-      float top = -INFINITY;
+      for (int h = 0; h < kDecHeads; ++h) acc[0][h] = acc[1][h] = f2(0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < KK / 4; ++g) {
-        float d[32];
+      for (int c = 0; c < D / 32; ++c) {
+        F2 ka, kb, kc, kd;
+        lds(st + (4 * g + kg) * S::kRow + 16 * (j + 8 * c), ka, kb);
+        lds(st + (4 * g + 4 + kg) * S::kRow + 16 * (j + 8 * c), kc, kd);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float x[E];
-          dec_row<E>(st + (4 * g + k) * S::kRow, lane, x);
+        for (int h = 0; h < kDecHeads; ++h) {
+          F2 qa, qb;
+          lds(&sh.q[h][4 * (j + 8 * c)], qa, qb);
+          acc[0][h] = fma2(ka, qa, acc[0][h]);
+          acc[0][h] = fma2(kb, qb, acc[0][h]);
+          acc[1][h] = fma2(kc, qa, acc[1][h]);
+          acc[1][h] = fma2(kd, qb, acc[1][h]);
+        }
+      }
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            float acc = 0.f;
+      for (int x = 0; x < 2; ++x) {
+        float d[kDecHeads];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc = fmaf(q[h][e], x[e], acc);
-            d[k * 8 + h] = acc;
-          }
+        for (int h = 0; h < kDecHeads; ++h) {
+          const float2 v = unpack(acc[x][h]);
+          d[h] = v.x + v.y;
         }
         // halve the values while folding the lanes: lane bit w keeps the half with that bit
 #pragma unroll
-        for (int w = 16; w >= 1; w >>= 1) {
+        for (int w = 4; w >= 1; w >>= 1) {
 #pragma unroll
-          for (int j = 0; j < w; ++j) {
+          for (int k = 0; k < w; ++k) {
             const bool up = lane & w;
-            const float keep = up ? d[j + w] : d[j], give = up ? d[j] : d[j + w];
-            d[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+            const float keep = up ? d[k + w] : d[k], give = up ? d[k] : d[k + w];
+            d[k] = keep + __shfl_xor_sync(0xffffffffu, give, w);
           }
         }
-        const bool ok = here >> (4 * g + (lane >> 3)) & 1;
-        z[g] = ok ? d[0] * a.scale_log2 : -INFINITY;
-        top = fmaxf(top, z[g]);
+        const bool ok = here >> (4 * (g + x) + kg) & 1;
+        z[g + x] = ok ? d[0] * a.scale_log2 : -INFINITY;
+        top = fmaxf(top, z[g + x]);
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      const float m_new = fmaxf(m, top);
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+    const float m_new = fmaxf(m, top);
+    const float m_use = m_new == -INFINITY ? 0.f : m_new;
+    if (__any_sync(0xffffffffu, m_new != m)) {
       const float alpha = exp2f(m - m_use);
       m = m_new;
       l *= alpha;
+      lm *= alpha;
 #pragma unroll
-      for (int g = 0; g < KK / 4; ++g) {
-        const float p = exp2f(z[g] - m_use);
-        l += p;
-        pbuf[warp][4 * g + (lane >> 3)][lane & 7] = p;
-      }
-      if (__any_sync(0xffffffffu, alpha != 1.f)) {
+      for (int h = 0; h < kDecHeads; ++h) {
+        const float f = __shfl_sync(0xffffffffu, alpha, h);
+        const F2 ff = f2(f, f);
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const float f = __shfl_sync(0xffffffffu, alpha, h);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[h][e] *= f;
+        for (int e = 0; e < E2; ++e) {
+          o[h][e] = mul2(o[h][e], ff);
+          om[h][e] = mul2(om[h][e], ff);
         }
       }
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < KK; ++k) {
-        float x[E];
-        dec_row<E>(st + (KK + k) * S::kRow, lane, x);
-        const float4 pa = *reinterpret_cast<const float4*>(&pbuf[warp][k][0]);
-        const float4 pb = *reinterpret_cast<const float4*>(&pbuf[warp][k][4]);
-        const float p[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-#pragma unroll
-        for (int h = 0; h < 8; ++h)
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[h][e] = fmaf(p[h], x[e], o[h][e]);
-      }
     }
-    cp_async_wait<0>();
-    l += __shfl_xor_sync(0xffffffffu, l, 8);
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
-    if (lane < 8) {
-      sh.m[warp][lane] = m;
-      sh.l[warp][lane] = l;
+#pragma unroll
+    for (int g = 0; g < KK / 4; ++g) {
+      const float p = exp2f(z[g] - m_use);
+      l += p;
+      sh.p[warp][4 * g + kg][j] = make_float2(p, p);
     }
     __syncwarp();
-    float* obuf = reinterpret_cast<float*>(ring);  // this warp's ring is at rest
 #pragma unroll
-    for (int h = 0; h < 8; ++h)
+    for (int k = 0; k < KK; ++k) {
+      const uint8_t* row = st + (KK + k) * S::kRow + lane * (8 * E2);
+      F2 x[E2];
+      if (E2 == 2)
+        lds(row, x[0], x[E2 - 1]);
+      else
+        x[0].v = *reinterpret_cast<const unsigned long long*>(row);
 #pragma unroll
-      for (int e = 0; e < E; ++e) obuf[h * D + lane * E + e] = o[h][e];
-    __syncthreads();
-    dec_end_run<T, D>(a, sh, smem, at, n_tiles, u, L, &join);
-    __syncthreads();
-    u += n_tiles;
-    dec_advance<S::kTile>(a, &at, &bits);
+      for (int h = 0; h < kDecHeads; h += 2) {
+        F2 pa, pb;
+        lds(&sh.p[warp][k][h], pa, pb);
+#pragma unroll
+        for (int e = 0; e < E2; ++e) {
+          o[h][e] = fma2(pa, x[e], o[h][e]);
+          o[h + 1][e] = fma2(pb, x[e], o[h + 1][e]);
+        }
+      }
+    }
+    if (++n == kFlush) flush();
   }
-  dec_end(a, sh, bits, join);
-}
+
+  __device__ __forceinline__ void flush() {
+    n = 0;
+    lm += l;
+    l = 0.f;
+#pragma unroll
+    for (int h = 0; h < kDecHeads; ++h)
+#pragma unroll
+      for (int e = 0; e < E2; ++e) {
+        om[h][e] = add2(om[h][e], o[h][e]);
+        o[h][e] = f2(0.f, 0.f);
+      }
+  }
+
+  __device__ __forceinline__ void sums(float (&ms)[kDecHeads], float (&ls)[kDecHeads]) {
+    flush();
+    lm += __shfl_xor_sync(0xffffffffu, lm, 8);
+    lm += __shfl_xor_sync(0xffffffffu, lm, 16);
+    if (lane < kDecHeads) {
+      ms[lane] = m;
+      ls[lane] = lm;
+    }
+  }
+  __device__ __forceinline__ void outputs(float* out) const {
+#pragma unroll
+    for (int h = 0; h < kDecHeads; ++h)
+#pragma unroll
+      for (int e = 0; e < E2; ++e)
+        *reinterpret_cast<float2*>(&out[h * (D + 4) + lane * 2 * E2 + 2 * e]) = unpack(om[h][e]);
+  }
+};
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const uint8_t* p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -470,189 +646,153 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 
 // bf16: keys fill the rows of a product's tile and 8 query heads its columns,
 //   S^T [16 keys x 8 heads] = K Q^T,   O^T [16 d x 8 heads] += V^T P^T,
-// so that no part of a tile is padding when a KV head serves 8 query heads (128
-// rows of tcgen05 would hold 7 or 8 of them), and a lane's softmax columns are
-// its output columns. P goes to the second product as two bf16 parts (high and
-// rest: 2^-17 relative), which costs 8 more products per 16 keys and keeps the
-// output as near as fp32 weights would. The warp's keys pass through a ring of
-// stages of its own (cp.async), the table entry of a stage one step ahead.
+// so that no part of a tile is padding when a KV head serves 8 query heads (the
+// 128 rows of a tcgen05 tile would hold 7 or 8 of them), and a lane's softmax
+// columns are its output columns. P goes to the second product as two bf16 parts
+// (high and rest: 2^-17 relative), which costs 8 more products per 16 keys and
+// keeps the output as near as fp32 weights would.
 template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32) decode_mma_kernel(const DecodeArgs a) {
-  using T = __nv_bfloat16;
-  using S = DecShape<T, D>;
-  constexpr int KK = S::kKeys, MT = KK / 16, DT = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ DecShared sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  dependency_release();
-  uint32_t bits = 0;
-  const DecLine L = dec_begin<T, D>(a, sh, &bits);
-  int4 join = make_int4(-1, 0, 0, 0);
-  DecSpot at = sh.first;
-  uint8_t* ring = smem + warp * S::kRing;
-  for (long long u = L.u0; u < L.u1;) {
-    const int n_tiles = (int)min((long long)(at.tiles - at.tile), L.u1 - u);
+struct DecBf16 {
+  using S = DecShape<__nv_bfloat16, D>;
+  static constexpr int KK = S::kKeys, MT = KK / 16, DT = D / 16;
+  struct Shared {};
+  const DecodeArgs& a;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  uint32_t qf[DT][2];
+  float o[DT][4];
+  float m0, m1, l0, l1;  // heads 2c, 2c + 1
+
+  __device__ __forceinline__ DecBf16(const DecodeArgs& a_, Shared&) : a(a_) {}
+
+  __device__ __forceinline__ void begin(const DecSpot& at) {
     const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
     const int heads = min(kDecHeads, a.group - hg * kDecHeads);
-    const int h0 = kvh * a.group + hg * kDecHeads;
-    const int32_t* pages = a.table + at.seq * a.table_stride;
-    const int key0 = at.tile * S::kTile + warp * KK + lane;  // of this lane's row, stage 0
-    auto entry = [&](int i) -> int {
-      const int key = key0 + i * S::kTile;
-      return i < n_tiles && lane < KK && key < at.len ? pages[key / a.cs.page_size] : 0;
-    };
-    auto fetch = [&](int i, int page) -> uint32_t {
-      const int64_t off = i < n_tiles && lane < KK
-                              ? dec_offset(a, key0 + i * S::kTile, at.len, page, kvh, &bits)
-                              : -1;
-      dec_copy<T, D>(a, ring + (i % kDecStages) * S::kStage, off, i < n_tiles);
-      return __ballot_sync(0xffffffffu, off >= 0);
-    };
-    uint32_t there[kDecStages];
-    int page[kDecStages];
-#pragma unroll
-    for (int i = 0; i < kDecStages; ++i) page[i] = entry(i);
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) there[i] = fetch(i, page[i]);
-    int ahead = page[kDecStages - 1];
     // Q^T: column g is head g, rows 2c, 2c + 1 and 8 further of each 16 of d
-    uint32_t qf[DT][2];
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + at.seq * a.qs.ts +
+                             (int64_t)(kvh * a.group + hg * kDecHeads + g) * a.qs.hs + 2 * c;
 #pragma unroll
     for (int k = 0; k < DT; ++k) {
-      qf[k][0] = qf[k][1] = 0u;
-      if (g < heads) {
-        const T* p = static_cast<const T*>(a.q) + at.seq * a.qs.ts + (h0 + g) * a.qs.hs + 16 * k +
-                     2 * c;
-        qf[k][0] = *reinterpret_cast<const uint32_t*>(p);
-        qf[k][1] = *reinterpret_cast<const uint32_t*>(p + 8);
-      }
-    }
-    float o[DT][4];
-#pragma unroll
-    for (int k = 0; k < DT; ++k)
+      qf[k][0] = g < heads ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
+      qf[k][1] = g < heads ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
+    }
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  }
 
-    for (int i = 0; i < n_tiles; ++i) {
-      __syncwarp();  // the stage that is fetched into was read by every lane
-      const uint32_t next = fetch(i + kDecStages - 1, ahead);
-      ahead = entry(i + kDecStages);
-      cp_async_wait<kDecStages - 1>();
-      __syncwarp();
-      const uint32_t here = there[0];
+  __device__ __forceinline__ void tile(const uint8_t* st, uint32_t here) {
+    // scores: rows g and g + 8 of each 16 keys, heads 2c and 2c + 1
+    float z[MT][4];
+    float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-      for (int k = 0; k + 1 < kDecStages - 1; ++k) there[k] = there[k + 1];
-      there[kDecStages - 2] = next;
-      const uint8_t* st = ring + (i % kDecStages) * S::kStage;
-      // scores: rows g and g + 8 of each 16 keys, heads 2c and 2c + 1
-      float z[MT][4];
-      float t0 = -INFINITY, t1 = -INFINITY;
+    for (int t = 0; t < MT; ++t) {
+      float s0[4] = {}, s1[4] = {};  // even and odd steps: two shorter chains
+      const uint8_t* row = st + (16 * t + (lane & 15)) * S::kRow + (lane >> 4) * 16;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        float s0[4] = {}, s1[4] = {};  // even and odd steps: two shorter chains
-        const uint8_t* row = st + (16 * t + (lane & 15)) * S::kRow + (lane >> 4) * 16;
-#pragma unroll
-        for (int k = 0; k < DT; ++k) {
-          uint32_t f[4];
-          ldmatrix4(f, row + k * 32);
-          if (k & 1)
-            mma_16816(s1, f, qf[k][0], qf[k][1]);
-          else
-            mma_16816(s0, f, qf[k][0], qf[k][1]);
-        }
-        const bool lo = here >> (16 * t + g) & 1, hi = here >> (16 * t + g + 8) & 1;
-        z[t][0] = lo ? (s0[0] + s1[0]) * a.scale_log2 : -INFINITY;
-        z[t][1] = lo ? (s0[1] + s1[1]) * a.scale_log2 : -INFINITY;
-        z[t][2] = hi ? (s0[2] + s1[2]) * a.scale_log2 : -INFINITY;
-        z[t][3] = hi ? (s0[3] + s1[3]) * a.scale_log2 : -INFINITY;
-        t0 = fmaxf(t0, fmaxf(z[t][0], z[t][2]));
-        t1 = fmaxf(t1, fmaxf(z[t][1], z[t][3]));
+      for (int k = 0; k < DT; ++k) {
+        uint32_t f[4];
+        ldmatrix4(f, row + k * 32);
+        if (k & 1)
+          mma_16816(s1, f, qf[k][0], qf[k][1]);
+        else
+          mma_16816(s0, f, qf[k][0], qf[k][1]);
       }
+      const bool lo = here >> (16 * t + g) & 1, hi = here >> (16 * t + g + 8) & 1;
+      z[t][0] = lo ? (s0[0] + s1[0]) * a.scale_log2 : -INFINITY;
+      z[t][1] = lo ? (s0[1] + s1[1]) * a.scale_log2 : -INFINITY;
+      z[t][2] = hi ? (s0[2] + s1[2]) * a.scale_log2 : -INFINITY;
+      z[t][3] = hi ? (s0[3] + s1[3]) * a.scale_log2 : -INFINITY;
+      t0 = fmaxf(t0, fmaxf(z[t][0], z[t][2]));
+      t1 = fmaxf(t1, fmaxf(z[t][1], z[t][3]));
+    }
 #pragma unroll
-      for (int w = 4; w <= 16; w <<= 1) {
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+    for (int w = 4; w <= 16; w <<= 1) {
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+    }
+    t0 = fmaxf(t0, m0);
+    t1 = fmaxf(t1, m1);
+    const float u0 = t0 == -INFINITY ? 0.f : t0, u1 = t1 == -INFINITY ? 0.f : t1;
+    if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {
+      const float f0 = exp2f(m0 - u0), f1 = exp2f(m1 - u1);
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int k = 0; k < DT; ++k) {
+        o[k][0] *= f0; o[k][1] *= f1; o[k][2] *= f0; o[k][3] *= f1;
       }
-      t0 = fmaxf(t0, m0);
-      t1 = fmaxf(t1, m1);
-      const float u0 = t0 == -INFINITY ? 0.f : t0, u1 = t1 == -INFINITY ? 0.f : t1;
-      if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {
-        const float f0 = exp2f(m0 - u0), f1 = exp2f(m1 - u1);
-        l0 *= f0;
-        l1 *= f1;
+      m0 = t0;
+      m1 = t1;
+    }
 #pragma unroll
-        for (int k = 0; k < DT; ++k) {
-          o[k][0] *= f0; o[k][1] *= f1; o[k][2] *= f0; o[k][3] *= f1;
-        }
-        m0 = t0;
-        m1 = t1;
-      }
+    for (int t = 0; t < MT; ++t) {
+      const float p0 = exp2f(z[t][0] - u0), p1 = exp2f(z[t][1] - u1);
+      const float p2 = exp2f(z[t][2] - u0), p3 = exp2f(z[t][3] - u1);
+      l0 += p0 + p2;
+      l1 += p1 + p3;
+      const uint32_t ha = pack_bf16x2(p0, p1), hb = pack_bf16x2(p2, p3);
+      const uint32_t ra = pack_bf16x2(p0 - __uint_as_float(ha << 16),
+                                      p1 - __uint_as_float(ha & 0xffff0000u));
+      const uint32_t rb = pack_bf16x2(p2 - __uint_as_float(hb << 16),
+                                      p3 - __uint_as_float(hb & 0xffff0000u));
+      const uint32_t ph0 = movmatrix(ha), ph1 = movmatrix(hb);
+      const uint32_t pr0 = movmatrix(ra), pr1 = movmatrix(rb);
+      const uint8_t* row = st + (KK + 16 * t + (lane & 7) + (lane >> 4) * 8) * S::kRow +
+                           (lane >> 3 & 1) * 16;
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const float p0 = exp2f(z[t][0] - u0), p1 = exp2f(z[t][1] - u1);
-        const float p2 = exp2f(z[t][2] - u0), p3 = exp2f(z[t][3] - u1);
-        l0 += p0 + p2;
-        l1 += p1 + p3;
-        const uint32_t ha = pack_bf16x2(p0, p1), hb = pack_bf16x2(p2, p3);
-        const uint32_t ra = pack_bf16x2(p0 - __uint_as_float(ha << 16),
-                                        p1 - __uint_as_float(ha & 0xffff0000u));
-        const uint32_t rb = pack_bf16x2(p2 - __uint_as_float(hb << 16),
-                                        p3 - __uint_as_float(hb & 0xffff0000u));
-        const uint32_t ph0 = movmatrix(ha), ph1 = movmatrix(hb);
-        const uint32_t pr0 = movmatrix(ra), pr1 = movmatrix(rb);
-        const uint8_t* row = st + (KK + 16 * t + (lane & 7) + (lane >> 4) * 8) * S::kRow +
-                             (lane >> 3 & 1) * 16;
-#pragma unroll
-        for (int k = 0; k < DT; ++k) {
-          uint32_t f[4];
-          ldmatrix4_trans(f, row + k * 32);
-          mma_16816(o[k], f, ph0, ph1);
-          mma_16816(o[k], f, pr0, pr1);
-        }
+      for (int k = 0; k < DT; ++k) {
+        uint32_t f[4];
+        ldmatrix4_trans(f, row + k * 32);
+        mma_16816(o[k], f, ph0, ph1);
+        mma_16816(o[k], f, pr0, pr1);
       }
     }
-    cp_async_wait<0>();
+  }
+
+  __device__ __forceinline__ void sums(float (&ms)[kDecHeads], float (&ls)[kDecHeads]) {
 #pragma unroll
     for (int w = 4; w <= 16; w <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, w);
       l1 += __shfl_xor_sync(0xffffffffu, l1, w);
     }
     if (g == 0) {
-      sh.m[warp][2 * c] = m0;
-      sh.m[warp][2 * c + 1] = m1;
-      sh.l[warp][2 * c] = l0;
-      sh.l[warp][2 * c + 1] = l1;
+      ms[2 * c] = m0;
+      ms[2 * c + 1] = m1;
+      ls[2 * c] = l0;
+      ls[2 * c + 1] = l1;
     }
-    __syncwarp();
-    float* obuf = reinterpret_cast<float*>(ring);  // this warp's ring is at rest
+  }
+  __device__ __forceinline__ void outputs(float* out) const {
 #pragma unroll
     for (int k = 0; k < DT; ++k) {
-      obuf[2 * c * D + 16 * k + g] = o[k][0];
-      obuf[(2 * c + 1) * D + 16 * k + g] = o[k][1];
-      obuf[2 * c * D + 16 * k + g + 8] = o[k][2];
-      obuf[(2 * c + 1) * D + 16 * k + g + 8] = o[k][3];
+      float* p = out + 2 * c * (D + 4) + 16 * k + g;
+      p[0] = o[k][0];
+      p[D + 4] = o[k][1];
+      p[8] = o[k][2];
+      p[D + 12] = o[k][3];
     }
-    __syncthreads();
-    dec_end_run<T, D>(a, sh, smem, at, n_tiles, u, L, &join);
-    __syncthreads();
-    u += n_tiles;
-    dec_advance<S::kTile>(a, &at, &bits);
   }
-  dec_end(a, sh, bits, join);
-}
+};
 
-// Joins the parts of a run that was cut: one block per block of the first kernel (the run
-// that starts there and ends in a later one) and head. Block (0, 0) collects the status.
+// Joins the parts of a run that was cut: a block per entry of joins and head,
+// G groups of D threads that take every G-th part; a part's values are on their
+// way before the weights are known (65793 keys of one sequence come in some 100
+// parts: 28 us as a chain of dependent loads, 4 us so). Block (0, 0) collects the
+// status.
+constexpr int kJoinThreads = 512;
 template <typename T, int D>
-__global__ void __launch_bounds__(D) decode_join_kernel(const DecodeArgs a, int B) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a, int B) {
+  constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
+  __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  dependency_release();
   dependency_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == W - 1) {
     uint32_t v = 0;
-    for (int i = threadIdx.x; i < B; i += 32) v |= (uint32_t)a.status[i];
+    for (int i = lane; i < B; i += 32) v |= (uint32_t)a.status[i];
     v = __reduce_or_sync(0xffffffffu, v);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       a.hdr->status = v;
       a.hdr->detail = v ? 0x9100u : 0u;
     }
@@ -661,28 +801,56 @@ __global__ void __launch_bounds__(D) decode_join_kernel(const DecodeArgs a, int 
   if (j.x < 0) return;
   const int kvh = j.y / a.hgroups, hg = j.y % a.hgroups, h = blockIdx.y;
   if (h >= min(kDecHeads, a.group - hg * kDecHeads)) return;
-  auto part = [&](int slot) { return a.part + ((int64_t)slot * kDecHeads + h) * (D + 2); };
-  const int n = 1 + (j.w - (j.z & ~1)) / 2;        // slots j.z, then the next blocks' first ones
-  auto slot_of = [&](int i) { return i == 0 ? j.z : (j.z & ~1) + 2 * i; };
-  float mm = -INFINITY;
-  for (int i = 0; i < n; ++i) mm = fmaxf(mm, part(slot_of(i))[D]);
-  const float mu = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f, acc = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* p = part(slot_of(i));
-    const float f = exp2f(p[D] - mu);
-    ll = fmaf(p[D + 1], f, ll);
-    acc = fmaf(p[threadIdx.x], f, acc);
+  // slot j.z, then the next blocks' first ones
+  const int n = 1 + (j.w - (j.z & ~1)) / 2, b0 = j.z & ~1;
+  auto part = [&](int i) {
+    const int slot = i == 0 ? j.z : b0 + 2 * i;
+    return a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
+  };
+  const int e = tid % D, g = tid / D;
+  float early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) early[k] = g + G * k < n ? part(g + G * k)[e] : 0.f;
+  // n <= kDecMaxBlocks <= kJoinThreads: a part's maximum and sum per thread
+  static_assert(kDecMaxBlocks <= kJoinThreads, "");
+  float m = -INFINITY, l = 0.f;
+  if (tid < n) {
+    m = part(tid)[D];
+    l = part(tid)[D + 1];
   }
+  const float wm = warp_max(m);
+  if (lane == 0) red[0][warp] = wm;
+  __syncthreads();
+  float mm = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < W; ++w) mm = fmaxf(mm, red[0][w]);
+  const float mu = mm == -INFINITY ? 0.f : mm;
+  if (tid < n) {
+    f[tid] = exp2f(m - mu);
+    l *= f[tid];
+  }
+  const float wl = warp_sum(l);
+  if (lane == 0) red[1][warp] = wl;
+  __syncthreads();
+  float ll = 0.f, acc = 0.f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) ll += red[1][w];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (g + G * k < n) acc = fmaf(early[k], f[g + G * k], acc);
+#pragma unroll 4
+  for (int i = g + G * kEarly; i < n; i += G) acc = fmaf(part(i)[e], f[i], acc);
+  acc_g[g][e] = acc;
+  __syncthreads();
+  if (g) return;
+#pragma unroll
+  for (int i = 1; i < G; ++i) acc += acc_g[i][e];
   const int64_t row = (int64_t)j.x * a.hq + kvh * a.group + hg * kDecHeads + h;
-  static_cast<T*>(a.out)[row * D + threadIdx.x] = from_f32<T>(ll == 0.f ? 0.f : acc / ll);
-  if (a.lse && threadIdx.x == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  static_cast<T*>(a.out)[row * D + e] = from_f32<T>(ll == 0.f ? 0.f : acc / ll);
+  if (a.lse && tid == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 namespace {
-
-constexpr int kDecMaxBlocks = 148 * 2;
 
 struct DecLayout {
   size_t status, joins, part, total;
@@ -700,25 +868,29 @@ DecLayout dec_layout(int d) {
   return L;
 }
 
-template <typename T, int D>
-cudaError_t launch_decode(const DecodeArgs& a, void (*kernel)(DecodeArgs), int sms,
-                          cudaStream_t s) {
-  using S = DecShape<T, D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
+template <class M>
+int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
+  using S = typename M::S;
   // no more blocks than tiles the tables can hold
-  const int64_t tiles = (int64_t)a.n_seqs * a.hkv * a.hgroups *
-                        (((int64_t)a.max_len + S::kTile - 1) / S::kTile);
-  int64_t grid = 2 * (int64_t)sms;
+  const int64_t runs = (int64_t)a.n_seqs * a.hkv * a.hgroups;
+  const int64_t tiles = runs * (((int64_t)a.max_len + S::kTile - 1) / S::kTile);
+  if (tiles > INT32_MAX) return ADASPARK_EINVAL;
+  int64_t grid = S::kBlocks * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;
   if (grid > tiles) grid = tiles;
-  const cudaError_t r = launch("decode_attn", kernel, dim3((unsigned)grid), dim3(kDecWarps * 32),
-                               S::kSmem, s, a);
-  if (r != cudaSuccess) return r;
+  a.by_run = runs <= grid;
+  a.in_page = a.cs.page_size % S::kKeys == 0;
+  a.tile_pages = S::kTile / a.cs.page_size;
+  a.tile_rest = S::kTile % a.cs.page_size;
+  int rc = allow_smem(decode_kernel<M>, S::kSmem);
+  if (rc == ADASPARK_OK)
+    rc = cuda_status(launch_after("decode_attn", decode_kernel<M>, dim3((unsigned)grid),
+                                  dim3(kDecWarps * 32), S::kSmem, s, a));
+  if (rc != ADASPARK_OK) return rc;
   const int heads = a.group < kDecHeads ? a.group : kDecHeads;
-  return launch_after("decode_join", decode_join_kernel<T, D>, dim3((unsigned)grid, heads), dim3(D),
-                      0, s, a, (int)grid);
+  return cuda_status(launch_after("decode_join", decode_join_kernel<typename S::T, S::D>,
+                                  dim3((unsigned)(a.by_run ? runs : grid), heads),
+                                  dim3(kJoinThreads), 0, s, a, (int)grid));
 }
 
 }  // namespace
@@ -771,11 +943,8 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   a.part = reinterpret_cast<float*>(ws + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == ADASPARK_BF16)
-    return cuda_status(
-        d == 128 ? launch_decode<__nv_bfloat16, 128>(a, decode_mma_kernel<128>, sms, s)
-                 : launch_decode<__nv_bfloat16, 64>(a, decode_mma_kernel<64>, sms, s));
-  return cuda_status(d == 128 ? launch_decode<float, 128>(a, decode_simt_kernel<128>, sms, s)
-                              : launch_decode<float, 64>(a, decode_simt_kernel<64>, sms, s));
+    return d == 128 ? launch_decode<DecBf16<128>>(a, sms, s) : launch_decode<DecBf16<64>>(a, sms, s);
+  return d == 128 ? launch_decode<DecFp32<128>>(a, sms, s) : launch_decode<DecFp32<64>>(a, sms, s);
 }
 
 }  // extern "C"

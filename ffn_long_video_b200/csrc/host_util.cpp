@@ -96,6 +96,28 @@ int device_is_sm100() {
   return (major == 10 && minor == 0) ? 1 : 0;
 }
 
+int allow_smem(const void* kernel, int bytes) {
+  struct Known {
+    const void* kernel;
+    int device, bytes;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ADASPARK_ECUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Known& k : known)
+    if (k.kernel == kernel && k.device == dev && k.bytes >= bytes) return ADASPARK_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return ADASPARK_ECUDA;
+  try {
+    known.push_back({kernel, dev, bytes});
+  } catch (...) {  // not remembered: asked again next time
+  }
+  return ADASPARK_OK;
+}
+
 int current_device(int* sms) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> known[kMaxDevices] = {};  // SM count of an sm_100 device, -1 of another

@@ -30,6 +30,14 @@ inline cudaError_t launch(const char* name, void (*kernel)(KArgs...), dim3 grid,
   return e;
 }
 
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; asked
+// of the runtime once per kernel and device.
+int allow_smem(const void* kernel, int bytes);
+template <typename... KArgs>
+inline int allow_smem(void (*kernel)(KArgs...), int bytes) {
+  return allow_smem(reinterpret_cast<const void*>(kernel), bytes);
+}
+
 // launch() of a kernel whose blocks may come up while the stream's previous
 // kernel still runs: it must call dependency_wait() (common.cuh) before it
 // touches anything that kernel writes.

@@ -634,7 +634,8 @@ size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dt
  * Results depend on the inputs, the sizes and max_pages alone (no atomics). A
  * length out of range counts as 0 and a page number outside [0, n_pages) as
  * absent keys; both report ADASPARK_DEV_BAD_LAYOUT. Errors: ADASPARK_EINVAL as
- * for the other calls, or n_seqs or max_pages < 1. */
+ * for the other calls, n_seqs or max_pages < 1, or tables that could hold 2^31
+ * tiles of 32 keys and 8 query heads, over all sequences and KV heads. */
 int adaspark_decode_attn(const void *Q, int64_t q_ts, int64_t q_hs, const void *k_cache,
                          const void *v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,
                          int n_pages, int page_size, int dtype, const int32_t *block_table,
