@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  Torch tensors supply device memory and the current CUDA stream.  The
-binding fails loudly when the library is missing; there is no fallback.
+calls go through ctypes, those of generation through the extension module _calls
+(binding/calls.cpp).  The binding fails loudly when the library or the module is
+missing; there is no fallback.
 
 Entry points (same names as include/adaspark.h, without the prefix):
 ``cube_count``, ``cube_partition``, ``cube_attn`` (and ``_train``), ``cube_attn_topk``,
@@ -20,7 +22,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 import numpy as np
 
@@ -520,128 +521,33 @@ def rmsnorm(x, weight=None, eps=1e-6, out=None, stream=None):
 
 # ----------------------------------------------------------------- generation
 # These calls run once per layer and generated token, where a call's host time
-# counts: one check per property, no objects built on the way.
-def _elsewhere(device, stream):
-    """Context of a call on `stream`, or on a device that is not the current
-    one: what the call allocates then belongs to the stream that uses it."""
+# counts: checks, allocation and the C call are one step in binding/calls.cpp.
+_binding = None
+
+
+def _load_calls():
+    """The loaded _calls module (raises if it has not been built)."""
+    global _binding
+    lib()
+    import torch  # noqa: F401  (its libraries must be loaded first)
+    try:
+        from . import _calls as mod
+    except ImportError as e:
+        raise ImportError(
+            "ffn_long_video_b200/_calls.so is missing or does not load: build it with "
+            f"`python -m ffn_long_video_b200._build` (there is no fallback path): {e}") from e
+    mod.set_error(AdasparkError)
+    _binding = mod
+    return mod
+
+
+def _on(stream, t, name):
+    """Makes `stream` the current one for a call on `t`'s device, so that what the
+    call allocates belongs to the stream that uses it."""
     import torch
-    if device.type != "cuda":
-        raise ValueError(f"the tensors must be CUDA tensors, got {device}")
-    if stream is None:
-        return torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, {name} on {t.device}")
     return torch.cuda.stream(stream)
-
-
-# Layout of each call's words: integers and pointers q, floating point d, in the
-# order of the C prototype (sections by value).
-_ROPE_WORDS = "qq3qqqqdqqd"
-_WORDS = {
-    "qk_rope": "3q3qq" + _ROPE_WORDS + "4q3q3qq",
-    "qk_rope_append": "3q3q3qq" + _ROPE_WORDS + "4qq7q3qq",
-    "kv_append": "3q3q4qq7qq",
-    "qk_rope_backward": "3q3qq3q3qq" + _ROPE_WORDS + "4q4q2qq",
-    "kv_plan": "4q3q2q4qq2qq",
-    "decode_attn": "3q7qq3qq4qd2q2qq",
-}
-_packed_calls = {}
-
-
-def _packed(name, *args):
-    """The C call `name` with its arguments as words (csrc/packed.cpp)."""
-    call = _packed_calls.get(name)
-    if call is None:
-        fn = getattr(lib(), "adaspark_packed_" + name)
-        fn.restype, fn.argtypes = ctypes.c_int, [ctypes.c_char_p]
-        call = _packed_calls[name] = (struct.Struct("=" + _WORDS[name]).pack, fn)
-    return call[1](call[0](*args))
-
-
-def _refuse(t, name, dtype, gpu, shape):
-    where = "a CUDA tensor" if gpu < 0 or not t.is_cuda else f"on cuda:{gpu}"
-    raise ValueError(f"{name} must be {dtype} {tuple(shape)}, {where}; got {t.dtype} "
-                     f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
-
-
-def _rows(t, name, dtype, gpu, shape):
-    """Pointer, token stride and head stride of a [tokens, heads, d] tensor."""
-    if t.dtype is not dtype or t.get_device() != gpu or t.shape != shape:
-        _refuse(t, name, dtype, gpu, shape)
-    ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return t.data_ptr(), ts, hs
-
-
-def _flat(t, name, dtype, gpu, shape):
-    """Pointer of a dense tensor of the given shape."""
-    if (t.dtype is not dtype or t.get_device() != gpu or t.shape != shape
-            or not t.is_contiguous()):
-        _refuse(t, name, dtype, gpu, shape)
-    return t.data_ptr()
-
-
-def _heads(t, name):
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, d], got {tuple(t.shape)}")
-    return t.shape
-
-
-def _bytes(t, gpu):
-    """Pointer and bytes of a workspace."""
-    import torch
-    if t.dtype is not torch.uint8 or t.get_device() != gpu or not t.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{gpu}")
-    return t.data_ptr(), t.numel()
-
-
-def _table(t, gpu, n):
-    """Pointer, row stride and entries of a block table."""
-    import torch
-    if (t.dtype is not torch.int32 or t.get_device() != gpu or t.dim() != 2 or t.shape[0] != n
-            or (t.stride(1) != 1 and t.shape[1] > 1)):
-        raise ValueError(f"block_table must be int32 [{n}, max_pages] on cuda:{gpu}, rows "
-                         f"contiguous; got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr(), t.stride(0), t.shape[1]
-
-
-def _rope_args(n, d, dtype, gpu, positions, freq, w_q, w_k, eps, interleaved, sections, magnitude):
-    """positions, axes, three sections, freq, rot, interleaved, magnitude, w_q, w_k, eps."""
-    import torch
-    wq = 0 if w_q is None else _flat(w_q, "w_q", dtype, gpu, (d,))
-    wk = 0 if w_k is None else _flat(w_k, "w_k", dtype, gpu, (d,))
-    il = 1 if interleaved else 0
-    if freq is None:
-        return 0, 1, 0, 0, 0, 0, 0, il, magnitude, wq, wk, eps
-    if positions is None:
-        raise ValueError("positions is required")
-    half = freq.numel()
-    fr = _flat(freq, "freq", torch.float64, gpu, (half,))
-    if sections is None:
-        pos = _flat(positions, "positions", torch.int32, gpu, (n,))
-        return pos, 1, 0, 0, 0, fr, 2 * half, il, magnitude, wq, wk, eps
-    if len(sections) != 3:
-        raise ValueError("sections must be three numbers of pairs")
-    pos = _flat(positions, "positions", torch.int32, gpu, (3, n))
-    return (pos, 3, *sections, fr, 2 * half, il, magnitude, wq, wk, eps)
-
-
-def _cache_args(k_cache, v_cache, hkv, d, dtype, gpu):
-    """k, v, strides, pages and page size of a [pages, page_size, hkv, d] cache."""
-    shape = k_cache.shape
-    if len(shape) != 4:
-        raise ValueError(f"k_cache must be [pages, page_size, hkv, d], got {tuple(shape)}")
-    want = (shape[0], shape[1], hkv, d)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype is not dtype or t.get_device() != gpu or t.shape != want:
-            _refuse(t, name, dtype, gpu, want)
-    strides = k_cache.stride()
-    if strides[3] != 1 or v_cache.stride() != strides:
-        raise ValueError("k_cache and v_cache must have the same strides, with the elements of a "
-                         "head contiguous")
-    return (k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2], shape[0],
-            shape[1])
 
 
 def rope_frequencies(rot, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_len=0):
@@ -660,75 +566,38 @@ def qk_rope(Q, K, positions, freq, w_q=None, w_k=None, eps=1e-6, interleaved=Fal
             magnitude=1.0, out_q=None, out_k=None, stream=None):
     """Per-head RMSNorm (with ``w_q`` / ``w_k``) and rotary positions of Q
     [N, hq, d] and K [N, hkv, d] (any token and head strides): returns the
-    rotated (Q, K). ``freq`` float64 [rot/2] on the device, ``positions`` int32
-    [N], or [3, N] with ``sections`` (pairs per axis). ``out_q`` / ``out_k`` may be
-    Q / K themselves."""
-    import torch
-    gpu = Q.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(Q.device, stream):
+    rotated (Q, K). ``freq`` float64 [rot/2] on the device (None: nothing is
+    rotated), ``positions`` int32 [N], or [3, N] with ``sections`` (pairs per
+    axis). ``out_q`` / ``out_k`` may be Q / K themselves."""
+    if stream is not None:
+        with _on(stream, Q, "Q"):
             return qk_rope(Q, K, positions, freq, w_q, w_k, eps, interleaved, sections, magnitude,
                            out_q, out_k)
-    dt, code = Q.dtype, _dtype_code(Q)
-    n, hq, d = qs = _heads(Q, "Q")
-    ks = (n, _heads(K, "K")[1], d)
-    args = _rope_args(n, d, dt, gpu, positions, freq, w_q, w_k, eps, interleaved, sections,
-                      magnitude)
-    if out_q is None:
-        out_q = Q.new_empty(qs)
-    if out_k is None:
-        out_k = K.new_empty(ks)
-    rc = _packed("qk_rope", *_rows(Q, "Q", dt, gpu, qs), *_rows(K, "K", dt, gpu, ks), code,
-                                *args, n, hq, ks[1], d, *_rows(out_q, "out_q", dt, gpu, qs),
-                                *_rows(out_k, "out_k", dt, gpu, ks),
-                                torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_qk_rope")
-    return out_q, out_k
+    return (_binding or _load_calls()).qk_rope(Q, K, positions, freq, w_q, w_k, eps, interleaved,
+                                             sections, magnitude, out_q, out_k)
 
 
 def qk_rope_append(Q, K, V, positions, freq, slots, k_cache, v_cache, w_q=None, w_k=None, eps=1e-6,
                    interleaved=False, sections=None, magnitude=1.0, out_q=None, stream=None):
     """qk_rope of a step's tokens with the rotated keys, and V, written into the
-    paged cache [pages, page_size, hkv, d] at ``slots`` int32 [N] (-1: not
-    cached); returns the rotated Q."""
-    import torch
-    gpu = Q.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(Q.device, stream):
+    paged cache [pages, page_size, hkv, d] (any outer strides) at ``slots`` int32
+    [N] (-1: not cached); returns the rotated Q."""
+    if stream is not None:
+        with _on(stream, Q, "Q"):
             return qk_rope_append(Q, K, V, positions, freq, slots, k_cache, v_cache, w_q, w_k, eps,
                                   interleaved, sections, magnitude, out_q)
-    dt, code = Q.dtype, _dtype_code(Q)
-    n, hq, d = qs = _heads(Q, "Q")
-    hkv = _heads(K, "K")[1]
-    ks = (n, hkv, d)
-    args = _rope_args(n, d, dt, gpu, positions, freq, w_q, w_k, eps, interleaved, sections,
-                      magnitude)
-    if out_q is None:
-        out_q = Q.new_empty(qs)
-    rc = _packed("qk_rope_append", 
-        *_rows(Q, "Q", dt, gpu, qs), *_rows(K, "K", dt, gpu, ks), *_rows(V, "V", dt, gpu, ks), code,
-        *args, n, hq, hkv, d, _flat(slots, "slots", torch.int32, gpu, (n,)),
-        *_cache_args(k_cache, v_cache, hkv, d, dt, gpu), *_rows(out_q, "out_q", dt, gpu, qs),
-        torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_qk_rope_append")
-    return out_q
+    return (_binding or _load_calls()).qk_rope_append(Q, K, V, positions, freq, slots, k_cache,
+                                                    v_cache, w_q, w_k, eps, interleaved, sections,
+                                                    magnitude, out_q)
 
 
 def kv_append(K, V, slots, k_cache, v_cache, stream=None):
     """K and V [N, hkv, d] as they are into the paged cache at ``slots`` (-1: not
     cached)."""
-    import torch
-    gpu = K.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(K.device, stream):
+    if stream is not None:
+        with _on(stream, K, "K"):
             return kv_append(K, V, slots, k_cache, v_cache)
-    dt, code = K.dtype, _dtype_code(K)
-    n, hkv, d = ks = _heads(K, "K")
-    rc = _packed("kv_append", 
-        *_rows(K, "K", dt, gpu, ks), *_rows(V, "V", dt, gpu, ks), code, n, hkv, d,
-        _flat(slots, "slots", torch.int32, gpu, (n,)),
-        *_cache_args(k_cache, v_cache, hkv, d, dt, gpu), torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_kv_append")
+    return (_binding or _load_calls()).kv_append(K, V, slots, k_cache, v_cache)
 
 
 def qk_rope_backward_workspace_bytes(n_tokens, hq, hkv, d, dtype=BF16) -> int:
@@ -741,57 +610,14 @@ def qk_rope_backward(dQ_out, dK_out, positions, freq, Q=None, K=None, w_q=None, 
     """Backward of qk_rope: upstream gradients (bf16 or fp32) of its outputs;
     Q and K are its inputs, needed where a weight is given. Returns (dQ, dK,
     dw_q, dw_k, workspace), fp32; dw_q / dw_k are None without their weight."""
-    import torch
-    gpu = dQ_out.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(dQ_out.device, stream):
+    if stream is not None:
+        with _on(stream, dQ_out, "dQ_out"):
             return qk_rope_backward(dQ_out, dK_out, positions, freq, Q, K, w_q, w_k, eps,
                                     interleaved, sections, magnitude, dQ, dK, dw_q, dw_k,
                                     workspace)
-    f32 = torch.float32
-    dy, dy_code = dQ_out.dtype, _dtype_code(dQ_out)
-    n, hq, d = qs = _heads(dQ_out, "dQ_out")
-    hkv = _heads(dK_out, "dK_out")[1]
-    ks = (n, hkv, d)
-    w = w_q if w_q is not None else w_k
-    dt, code = (dy, dy_code) if w is None else (w.dtype, _dtype_code(w))
-    q = k = (0, 0, 0)
-    if w_q is not None:
-        if Q is None:
-            raise ValueError("Q is required with w_q")
-        q = _rows(Q, "Q", dt, gpu, qs)
-    if w_k is not None:
-        if K is None:
-            raise ValueError("K is required with w_k")
-        k = _rows(K, "K", dt, gpu, ks)
-    args = _rope_args(n, d, dt, gpu, positions, freq, w_q, w_k, eps, interleaved, sections,
-                      magnitude)
-    if dQ is None:
-        dQ = dQ_out.new_empty(qs, dtype=f32)
-    if dK is None:
-        dK = dK_out.new_empty(ks, dtype=f32)
-    if w_q is None:
-        dw_q = None
-    elif dw_q is None:
-        dw_q = w_q.new_empty((d,), dtype=f32)
-    if w_k is None:
-        dw_k = None
-    elif dw_k is None:
-        dw_k = w_k.new_empty((d,), dtype=f32)
-    if workspace is None and w is not None:
-        nb = qk_rope_backward_workspace_bytes(n, hq, hkv, d, code)
-        if nb == 0:
-            raise AdasparkError(EINVAL, "adaspark_qk_rope_backward_workspace")
-        workspace = w.new_empty((nb,), dtype=torch.uint8)
-    rc = _packed("qk_rope_backward", 
-        *_rows(dQ_out, "dQ_out", dy, gpu, qs), *_rows(dK_out, "dK_out", dy, gpu, ks), dy_code, *q,
-        *k, code, *args, n, hq, hkv, d, _flat(dQ, "dQ", f32, gpu, qs), _flat(dK, "dK", f32, gpu, ks),
-        0 if dw_q is None else _flat(dw_q, "dw_q", f32, gpu, (d,)),
-        0 if dw_k is None else _flat(dw_k, "dw_k", f32, gpu, (d,)),
-        *((0, 0) if workspace is None else _bytes(workspace, gpu)),
-        torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_qk_rope_backward")
-    return dQ, dK, dw_q, dw_k, workspace
+    return (_binding or _load_calls()).qk_rope_backward(
+        dQ_out, dK_out, positions, freq, Q, K, w_q, w_k, eps, interleaved, sections, magnitude,
+        dQ, dK, dw_q, dw_k, workspace)
 
 
 def kv_plan_workspace_bytes(n_seqs) -> int:
@@ -805,44 +631,13 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_ro
     ``n_free`` int32 [1] in place; returns (slots [n_rows], positions [n_rows],
     token_starts [n_seqs + 1], workspace). read_device_status(workspace) tells
     whether the plan was carried out."""
-    import torch
-    gpu = old_lens.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(old_lens.device, stream):
+    if stream is not None:
+        with _on(stream, old_lens, "old_lens"):
             return kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_rows,
                            slots, positions, token_starts, workspace)
-    i32 = torch.int32
-    ns, n_pages, n_rows = old_lens.numel(), free_pages.numel(), int(n_rows)
-    if slots is None and positions is None and token_starts is None and workspace is None:
-        # one allocation, the workspace first (256-byte aligned)
-        nb = kv_plan_workspace_bytes(ns)
-        if nb == 0 or n_rows < 1:
-            raise AdasparkError(EINVAL, "adaspark_kv_plan")
-        words = (nb // 4, n_rows, n_rows, ns + 1)
-        workspace, slots, positions, token_starts = old_lens.new_empty((sum(words),)).split(words)
-        workspace = workspace.view(torch.uint8)
-    if slots is None:
-        slots = old_lens.new_empty((n_rows,))
-    if positions is None:
-        positions = old_lens.new_empty((n_rows,))
-    if token_starts is None:
-        token_starts = old_lens.new_empty((ns + 1,))
-    if workspace is None:
-        nb = kv_plan_workspace_bytes(ns)
-        if nb == 0:
-            raise AdasparkError(EINVAL, "adaspark_kv_plan_workspace")
-        workspace = old_lens.new_empty((nb,), dtype=torch.uint8)
-    rc = _packed("kv_plan", 
-        _flat(old_lens, "old_lens", i32, gpu, (ns,)), _flat(new_lens, "new_lens", i32, gpu, (ns,)),
-        ns, int(page_size), *_table(block_table, gpu, ns),
-        _flat(free_pages, "free_pages", i32, gpu, (n_pages,)), n_pages,
-        _flat(n_free, "n_free", i32, gpu, (1,)),
-        _flat(token_starts, "token_starts", i32, gpu, (ns + 1,)),
-        _flat(slots, "slots", i32, gpu, (n_rows,)),
-        _flat(positions, "positions", i32, gpu, (n_rows,)), n_rows, *_bytes(workspace, gpu),
-        torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_kv_plan")
-    return slots, positions, token_starts, workspace
+    return (_binding or _load_calls()).kv_plan(old_lens, new_lens, block_table, free_pages, n_free,
+                                             page_size, n_rows, slots, positions, token_starts,
+                                             workspace)
 
 
 def decode_attn_workspace_bytes(n_seqs, hq, hkv, d, dtype=BF16) -> int:
@@ -855,34 +650,12 @@ def decode_attn(Q, k_cache, v_cache, block_table, seq_lens, scale=None, out=None
     cache [pages, page_size, hkv, d] (any outer strides): ``block_table`` int32
     [n_seqs, max_pages], ``seq_lens`` int32 [n_seqs]; ``scale`` defaults to
     1/sqrt(d). Returns (out, lse fp32 [n_seqs, hq], workspace)."""
-    import torch
-    gpu = Q.get_device()
-    if stream is not None or gpu < 0 or gpu != torch._C._cuda_getDevice():
-        with _elsewhere(Q.device, stream):
+    if stream is not None:
+        with _on(stream, Q, "Q"):
             return decode_attn(Q, k_cache, v_cache, block_table, seq_lens, scale, out, lse,
                                workspace)
-    dt, code = Q.dtype, _dtype_code(Q)
-    n, hq, d = qs = _heads(Q, "Q")
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages, page_size, hkv, d]")
-    hkv = k_cache.shape[2]
-    if out is None:
-        out = Q.new_empty(qs)
-    if lse is None:
-        lse = Q.new_empty((n, hq), dtype=torch.float32)
-    if workspace is None:
-        nb = decode_attn_workspace_bytes(n, hq, hkv, d, code)
-        if nb == 0:
-            raise AdasparkError(EINVAL, "adaspark_decode_attn_workspace")
-        workspace = Q.new_empty((nb,), dtype=torch.uint8)
-    rc = _packed("decode_attn", 
-        *_rows(Q, "Q", dt, gpu, qs), *_cache_args(k_cache, v_cache, hkv, d, dt, gpu), code,
-        *_table(block_table, gpu, n), _flat(seq_lens, "seq_lens", torch.int32, gpu, (n,)), n, hq,
-        hkv, d, d ** -0.5 if scale is None else scale, _flat(out, "out", dt, gpu, qs),
-        _flat(lse, "lse", torch.float32, gpu, (n, hq)), *_bytes(workspace, gpu),
-        torch._C._cuda_getCurrentRawStream(gpu))
-    _check(rc, "adaspark_decode_attn")
-    return out, lse, workspace
+    return (_binding or _load_calls()).decode_attn(Q, k_cache, v_cache, block_table, seq_lens, scale,
+                                                 out, lse, workspace)
 
 
 def ffn_export_active(workspace, n_tokens, n_vis, n_cubes, D, F, dtype, stream=None):

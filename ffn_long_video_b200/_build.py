@@ -1,10 +1,13 @@
-"""Build libadaspark.so in-tree with nvcc for sm_100a (no GPU needed).
+"""Build libadaspark.so in-tree with nvcc for sm_100a, and the Python binding of
+the generation calls, _calls.so, with the host compiler (no GPU needed).
 
     python -m ffn_long_video_b200._build [-v]
 
 Every .cu / .cpp under csrc/ is compiled separately (in parallel) into _build/
 and linked into ffn_long_video_b200/libadaspark.so.  The CUDA runtime is linked
 statically; the driver API is reached through cudaGetDriverEntryPoint.
+binding/calls.cpp is compiled against the installed torch and linked to
+libadaspark.so beside it.
 """
 from __future__ import annotations
 
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libadaspark.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -70,7 +74,40 @@ def build(verbose: bool = False, ptxas_v: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    build_calls(verbose)
     return LIB
+
+
+def build_calls(verbose: bool = False) -> str:
+    """_calls.so: the binding of the generation calls (needs libadaspark.so)."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(PKG, "binding", "calls.cpp")
+    troot = os.path.dirname(os.path.abspath(torch.__file__))
+    stamp = os.path.join(BUILD, "calls.torch")   # the torch it was compiled against
+    said = open(stamp).read() if os.path.exists(stamp) else ""
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "adaspark.h")))
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest and said == torch.__version__:
+        return CALLS
+    tlib = os.path.join(troot, "lib")
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(troot, "include"),
+           "-I", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), src, "-o", CALLS, "-L", PKG, "-l:libadaspark.so",
+           "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building _calls.so failed:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return CALLS
 
 
 if __name__ == "__main__":

@@ -25,12 +25,6 @@ namespace adaspark {
 #define DSB 3
 #define DBB 2
 #endif
-#ifndef DSF
-#define DSF 2
-#define DBF 3
-#define DSB 3
-#define DBB 2
-#endif
 struct DecodeArgs {
   WsHeader* hdr;
   const void* q;
@@ -82,8 +76,8 @@ struct DecShape {
   static constexpr int kTile = kKeys * kDecWarps;
   static constexpr int kRow = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 0);
   static constexpr int kStage = 2 * kKeys * kRow;            // K rows, V rows
-  static constexpr int kStages = sizeof(T) == 2 ? DSB : DSF;
-  static constexpr int kBlocks = sizeof(T) == 2 ? DBB : DBF;  // blocks per SM
+  static constexpr int kStages = 2;
+  static constexpr int kBlocks = sizeof(T) == 2 ? 2 : 3;     // blocks per SM
   static constexpr int kRing = kStages * kStage;
   static constexpr int kSmem = kDecWarps * kRing;
   static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
