@@ -184,6 +184,8 @@ __global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_kernel(const RopeArg
   constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
+  dependency_release();
+  dependency_wait();
   const int lane = threadIdx.x & 31;
   const int l = lane % M::kLanes, grp = lane / M::kLanes;
   const int heads = a.hq + a.hkv * (CACHE ? 2 : 1);
@@ -292,6 +294,8 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   constexpr int V = 4;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
+  dependency_release();
+  dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % M::kLanes, grp = lane / M::kLanes;
   const int heads = a.hq + a.hkv;
@@ -390,7 +394,6 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
     }
   }
   if constexpr (NORM) {
-    dependency_release();
     __shared__ float sum[4 * M::kHeads][2][D];
     float(*mine)[D] = sum[warp * M::kHeads + grp];
 #pragma unroll
@@ -415,8 +418,9 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
 // Sums the blocks' rows, 32 columns per block: column c of rows y, y + 32, ...
 __global__ void __launch_bounds__(1024)
     rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
-  dependency_wait();
   __shared__ float sum[32][33];
+  dependency_release();
+  dependency_wait();
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + x;
   float acc = 0.f;
@@ -485,8 +489,8 @@ cudaError_t launch_rope(RopeArgs a, bool il, int sms, cudaStream_t s) {
   const int64_t want = ((int64_t)a.n * a.parts + 3) / 4, most = (int64_t)sms * kRopeBlocks<T>;
   const dim3 grid((unsigned)(want < most ? want : most)), block(128);
   const char* name = CACHE ? "qk_rope_append" : "qk_rope";
-  if (il) return launch(name, rope_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a);
-  return launch(name, rope_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
+  if (il) return launch_after(name, rope_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a);
+  return launch_after(name, rope_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
 }
 
 template <typename T, int D, bool CACHE>
@@ -516,9 +520,9 @@ template <typename T, typename T2, int D, bool NORM>
 cudaError_t launch_bwd(const BwdCall& b, bool il, cudaStream_t s) {
   const dim3 grid(b.blocks), block(128);
   if (il)
-    return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, true, NORM>, grid, block, 0, s, b.a,
+    return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, true, NORM>, grid, block, 0, s, b.a,
                   b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
-  return launch("qk_rope_backward", rope_bwd_kernel<T, T2, D, false, NORM>, grid, block, 0, s, b.a,
+  return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, false, NORM>, grid, block, 0, s, b.a,
                 b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
 }
 
