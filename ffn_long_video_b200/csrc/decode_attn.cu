@@ -769,48 +769,125 @@ struct DecBf16 {
   }
 };
 
-// Joins the parts of a run that was cut: a block per entry of joins and head,
-// G groups of D threads that take every G-th part; a part's values are on their
-// way before the weights are known (65793 keys of one sequence come in some 100
-// parts: 28 us as a chain of dependent loads, 4 us so). Block (0, 0) collects the
-// status.
-constexpr int kJoinThreads = 512;
+// A cut run's parts for one head, and where its results go.
+template <int D>
+struct DecParts {
+  int n, first, rest;    // parts; slot of the first, then rest + 2 i
+  const float* part;
+  int64_t row;
+
+  __device__ __forceinline__ DecParts(const DecodeArgs& a, const int4& j, int h) {
+    n = 1 + (j.w - (j.z & ~1)) / 2;
+    first = j.z;
+    rest = j.z & ~1;
+    part = a.part + (int64_t)h * (D + 2);
+    row = (int64_t)j.x * a.hq + j.y / a.hgroups * a.group + j.y % a.hgroups * kDecHeads + h;
+  }
+  __device__ __forceinline__ const float* operator[](int i) const {
+    return part + (int64_t)(i == 0 ? first : rest + 2 * i) * (kDecHeads * (D + 2));
+  }
+};
+__device__ __forceinline__ int dec_heads_of(const DecodeArgs& a, const int4& j) {
+  return min(kDecHeads, a.group - j.y % a.hgroups * kDecHeads);
+}
+
+// Status of the call: what the blocks of the first kernel saw. One warp.
+__device__ __forceinline__ void dec_collect(const DecodeArgs& a, int B) {
+  uint32_t v = 0;
+  for (int i = threadIdx.x & 31; i < B; i += 32) v |= (uint32_t)a.status[i];
+  v = __reduce_or_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) {
+    a.hdr->status = v;
+    a.hdr->detail = v ? 0x9100u : 0u;
+  }
+}
+
+// Joins the parts of runs that were cut; two forms, both for any number of parts.
+// Few parts: a block per entry of joins, a warp per head; the first parts' values
+// are on their way before the weights are known.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeArgs a, int B) {
-  constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
-  __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a, int B) {
+  constexpr int E2 = D / 64, kEarly = 6;
+  const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
   dependency_release();
   dependency_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == W - 1) {
-    uint32_t v = 0;
-    for (int i = lane; i < B; i += 32) v |= (uint32_t)a.status[i];
-    v = __reduce_or_sync(0xffffffffu, v);
-    if (lane == 0) {
-      a.hdr->status = v;
-      a.hdr->detail = v ? 0x9100u : 0u;
+  if (blockIdx.x == 0 && h == kDecHeads - 1) dec_collect(a, B);
+  const int4 j = a.joins[blockIdx.x];
+  if (j.x < 0 || h >= dec_heads_of(a, j)) return;
+  const DecParts<D> p(a, j, h);
+  auto values = [&](int i, int e) {  // elements 64 e + 2 lane, + 1
+    return *reinterpret_cast<const float2*>(p[i] + 64 * e + 2 * lane);
+  };
+  float2 early[kEarly][E2];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+#pragma unroll
+    for (int e = 0; e < E2; ++e) early[k][e] = k < p.n ? values(k, e) : make_float2(0.f, 0.f);
+  // each lane a part's maximum and sum, 32 at a time
+  float mm = -INFINITY, ll = 0.f, acc[2 * E2] = {};
+  for (int i0 = 0; i0 < p.n; i0 += 32) {
+    const int i = i0 + lane;
+    const float m = i < p.n ? p[i][D] : -INFINITY, l = i < p.n ? p[i][D + 1] : 0.f;
+    const float m_new = fmaxf(mm, warp_max(m)), mu = m_new == -INFINITY ? 0.f : m_new;
+    const float scale = exp2f(mm - mu), f = i < p.n ? exp2f(m - mu) : 0.f;
+    mm = m_new;
+    ll = ll * scale + warp_sum(l * f);
+#pragma unroll
+    for (int e = 0; e < 2 * E2; ++e) acc[e] *= scale;
+    auto add = [&](int k, const float2 (&v)[E2]) {
+      const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+      for (int e = 0; e < E2; ++e) {
+        acc[2 * e] = fmaf(v[e].x, w, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(v[e].y, w, acc[2 * e + 1]);
+      }
+    };
+    int k = 0;
+    if (i0 == 0) {
+#pragma unroll
+      for (int x = 0; x < kEarly; ++x)
+        if (x < p.n) add(x, early[x]);
+      k = kEarly;
+    }
+    for (; k < min(32, p.n - i0); ++k) {
+      float2 v[E2];
+#pragma unroll
+      for (int e = 0; e < E2; ++e) v[e] = values(i0 + k, e);
+      add(k, v);
     }
   }
+#pragma unroll
+  for (int e = 0; e < 2 * E2; ++e)
+    static_cast<T*>(a.out)[p.row * D + 64 * (e / 2) + 2 * lane + e % 2] =
+        from_f32<T>(ll == 0.f ? 0.f : acc[e] / ll);
+  if (a.lse && lane == 0) a.lse[p.row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+}
+
+// Many parts: a block per entry of joins and head, G groups of D threads that take
+// every G-th part (65793 keys of one sequence come in 74 parts: 28 us as a chain of
+// dependent loads, 3 us so).
+constexpr int kJoinThreads = 512;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) decode_join_many_kernel(const DecodeArgs a, int B) {
+  constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
+  __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  dependency_release();
+  dependency_wait();
+  if (blockIdx.x == 0 && h == 0 && warp == W - 1) dec_collect(a, B);
   const int4 j = a.joins[blockIdx.x];
-  if (j.x < 0) return;
-  const int kvh = j.y / a.hgroups, hg = j.y % a.hgroups, h = blockIdx.y;
-  if (h >= min(kDecHeads, a.group - hg * kDecHeads)) return;
-  // slot j.z, then the next blocks' first ones
-  const int n = 1 + (j.w - (j.z & ~1)) / 2, b0 = j.z & ~1;
-  auto part = [&](int i) {
-    const int slot = i == 0 ? j.z : b0 + 2 * i;
-    return a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
-  };
+  if (j.x < 0 || h >= dec_heads_of(a, j)) return;
+  const DecParts<D> p(a, j, h);
   const int e = tid % D, g = tid / D;
   float early[kEarly];
 #pragma unroll
-  for (int k = 0; k < kEarly; ++k) early[k] = g + G * k < n ? part(g + G * k)[e] : 0.f;
+  for (int k = 0; k < kEarly; ++k) early[k] = g + G * k < p.n ? p[g + G * k][e] : 0.f;
   // n <= kDecMaxBlocks <= kJoinThreads: a part's maximum and sum per thread
   static_assert(kDecMaxBlocks <= kJoinThreads, "");
   float m = -INFINITY, l = 0.f;
-  if (tid < n) {
-    m = part(tid)[D];
-    l = part(tid)[D + 1];
+  if (tid < p.n) {
+    m = p[tid][D];
+    l = p[tid][D + 1];
   }
   const float wm = warp_max(m);
   if (lane == 0) red[0][warp] = wm;
@@ -819,7 +896,7 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
 #pragma unroll
   for (int w = 0; w < W; ++w) mm = fmaxf(mm, red[0][w]);
   const float mu = mm == -INFINITY ? 0.f : mm;
-  if (tid < n) {
+  if (tid < p.n) {
     f[tid] = exp2f(m - mu);
     l *= f[tid];
   }
@@ -831,17 +908,16 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeA
   for (int w = 0; w < W; ++w) ll += red[1][w];
 #pragma unroll
   for (int k = 0; k < kEarly; ++k)
-    if (g + G * k < n) acc = fmaf(early[k], f[g + G * k], acc);
+    if (g + G * k < p.n) acc = fmaf(early[k], f[g + G * k], acc);
 #pragma unroll 4
-  for (int i = g + G * kEarly; i < n; i += G) acc = fmaf(part(i)[e], f[i], acc);
+  for (int i = g + G * kEarly; i < p.n; i += G) acc = fmaf(p[i][e], f[i], acc);
   acc_g[g][e] = acc;
   __syncthreads();
   if (g) return;
 #pragma unroll
   for (int i = 1; i < G; ++i) acc += acc_g[i][e];
-  const int64_t row = (int64_t)j.x * a.hq + kvh * a.group + hg * kDecHeads + h;
-  static_cast<T*>(a.out)[row * D + e] = from_f32<T>(ll == 0.f ? 0.f : acc / ll);
-  if (a.lse && tid == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+  static_cast<T*>(a.out)[p.row * D + e] = from_f32<T>(ll == 0.f ? 0.f : acc / ll);
+  if (a.lse && tid == 0) a.lse[p.row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
 namespace {
@@ -881,10 +957,14 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
     rc = cuda_status(launch_after("decode_attn", decode_kernel<M>, dim3((unsigned)grid),
                                   dim3(kDecWarps * 32), S::kSmem, s, a));
   if (rc != ADASPARK_OK) return rc;
-  const int heads = a.group < kDecHeads ? a.group : kDecHeads;
-  return cuda_status(launch_after("decode_join", decode_join_kernel<typename S::T, S::D>,
-                                  dim3((unsigned)(a.by_run ? runs : grid), heads),
-                                  dim3(kJoinThreads), 0, s, a, (int)grid));
+  // Parts per run, about: from some 16 on their loads go side by side in a block.
+  const unsigned entries = (unsigned)(a.by_run ? runs : grid);
+  if (grid / runs >= 16)
+    return cuda_status(launch_after("decode_join", decode_join_many_kernel<typename S::T, S::D>,
+                                    dim3(entries, a.group < kDecHeads ? a.group : kDecHeads),
+                                    dim3(kJoinThreads), 0, s, a, (int)grid));
+  return cuda_status(launch_after("decode_join", decode_join_few_kernel<typename S::T, S::D>,
+                                  dim3(entries), dim3(32 * kDecHeads), 0, s, a, (int)grid));
 }
 
 }  // namespace

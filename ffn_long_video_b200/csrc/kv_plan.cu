@@ -41,6 +41,7 @@ constexpr int kPlanSeqs = 1024;      // sequences whose sums are kept in shared 
 // Up to here one block writes a plan's rows, 4 each thread: 64 sequences that gain 161
 // tokens 5.7 us against 7.8 for two kernels, 4096 rows 8.2 against 8.1.
 constexpr int kPlanOneBlock = 4096;
+constexpr int kPlanRows = 64;        // rows of a warp: 825 thousand in 12 us at 256, 5 at 64
 
 // Per-sequence values that the writes search, in shared memory or (more than
 // kPlanSeqs sequences) in global memory.
@@ -169,15 +170,15 @@ __device__ __forceinline__ int plan_taken(const PlanArgs& a, const PlanSums& p,
 }
 
 // Slots, positions, table and list entries, by `warps` warps of which this is `warp`. A warp
-// takes 256 rows at a time: one search for the first, then sequences and pages are followed.
+// takes kPlanRows rows at a time: one search for the first, then sequences and pages are
+// followed.
 __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
                                            const PlanTotals& t, int warp, int warps) {
   const int lane = threadIdx.x & 31, rows = t.ok ? t.rows : 0;
-  for (int r0 = warp * 256; r0 < a.n_rows; r0 += warps * 256) {
+  for (int r0 = warp * kPlanRows; r0 < a.n_rows; r0 += warps * kPlanRows) {
     int s = r0 < rows ? plan_find(p.starts, a.n_seqs, r0) : 0;
     int seen = -1, seen_s = -1, page = 0;
-#pragma unroll 2
-    for (int r = r0 + lane; r < min(r0 + 256, a.n_rows); r += 32) {
+    for (int r = r0 + lane; r < min(r0 + kPlanRows, a.n_rows); r += 32) {
       int slot = -1, pos = 0;
       if (r < rows) {
         while (s + 1 < a.n_seqs && p.starts[s + 1] <= r) ++s;
@@ -295,7 +296,8 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   cudaError_t e =
       launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e == cudaSuccess) {
-    const int64_t want = ((int64_t)n_rows + 2047) / 2048, most = (int64_t)sms * 4;
+    const int64_t want = ((int64_t)n_rows + 8 * kPlanRows - 1) / (8 * kPlanRows);
+    const int64_t most = (int64_t)sms * 8;
     const unsigned grid = (unsigned)(want < most ? want : most);
     e = launch_after("kv_plan_write", plan_write_kernel, dim3(grid), dim3(256), 0, s, a);
   }
