@@ -26,6 +26,7 @@ struct PlanArgs {
   int32_t *starts, *slots, *positions;
   int32_t *take0, *give0;        // workspace: pages taken / given by earlier sequences
   int32_t n_seqs, max_pages, page_size, n_pages, n_rows;
+  uint32_t div_mul, div_shift;   // n / page_size = n * div_mul >> div_shift for 0 <= n < 2^31
 };
 
 // Totals of a plan; the workspace header keeps them for the second kernel.
@@ -41,7 +42,6 @@ constexpr int kPlanSeqs = 1024;      // sequences whose sums are kept in shared 
 // Up to here one block writes a plan's rows, 4 each thread: 64 sequences that gain 161
 // tokens 5.7 us against 7.8 for two kernels, 4096 rows 8.2 against 8.1.
 constexpr int kPlanOneBlock = 4096;
-constexpr int kPlanRows = 64;        // rows of a warp: 825 thousand in 12 us at 256, 5 at 64
 
 // Per-sequence values that the writes search, in shared memory or (more than
 // kPlanSeqs sequences) in global memory.
@@ -53,8 +53,13 @@ struct PlanShared {
       starts[kPlanSeqs];
 };
 
-__device__ __forceinline__ int plan_pages(int n, int page_size) {
-  return n / page_size + (n % page_size != 0);
+__device__ __forceinline__ int plan_div(const PlanArgs& a, int n) {
+  return (int)((uint64_t)(uint32_t)n * a.div_mul >> a.div_shift);
+}
+// Pages of n tokens.
+__device__ __forceinline__ int plan_pages(const PlanArgs& a, int n) {
+  const int q = plan_div(a, n);
+  return q + (n != q * a.page_size);
 }
 
 // Inclusive sums of three values over the warp.
@@ -95,7 +100,7 @@ __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* s
       if (o < 0 || n < 0 || o > most || n > most) {
         bad = 1;
       } else {
-        const int po = plan_pages(o, a.page_size), pn = plan_pages(n, a.page_size);
+        const int po = plan_pages(a, o), pn = plan_pages(a, n);
         own[0] = max(pn - po, 0);
         own[1] = max(po - pn, 0);
         own[2] = max(n - o, 0);
@@ -156,59 +161,110 @@ __device__ __forceinline__ int plan_find(const int32_t* first, int n, int x) {
   return lo;
 }
 
-// The g-th page given back: from its sequence's table row, which this plan does not write there.
-__device__ __forceinline__ int plan_given(const PlanArgs& a, const PlanSums& p, int g) {
-  const int s = plan_find(p.give0, a.n_seqs, g);
-  const int col = plan_pages(p.new_lens[s], a.page_size) + g - p.give0[s];
+// The same for one x of a whole warp, 32 entries a step.
+__device__ __forceinline__ int plan_find_warp(const int32_t* first, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32, i = lane * step;
+    const uint32_t at_most = __ballot_sync(0xffffffffu, i < len && first[lo + min(i, len - 1)] <= x);
+    const int skip = max(__popc(at_most) - 1, 0) * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  return lo;
+}
+
+// The g-th page given back: from its sequence's table row, which this plan does not write
+// there. `s`: a sequence no later than the one it belongs to.
+__device__ __forceinline__ int plan_given(const PlanArgs& a, const PlanSums& p, int g, int s) {
+  while (s + 1 < a.n_seqs && p.give0[s + 1] <= g) ++s;
+  const int col = plan_pages(a, p.new_lens[s]) + g - p.give0[s];
   return a.table[s * a.table_stride + col];
 }
 
-// The t-th page taken. List entries from n_free on are written by this plan, those below are not.
+// The i-th page taken. List entries from n_free on are written by this plan, those below are not.
 __device__ __forceinline__ int plan_taken(const PlanArgs& a, const PlanSums& p,
-                                          const PlanTotals& t, int i) {
-  return i < t.give ? plan_given(a, p, i) : a.free_pages[t.n_free - 1 - (i - t.give)];
+                                          const PlanTotals& t, int i, int s) {
+  return i < t.give ? plan_given(a, p, i, s) : a.free_pages[t.n_free - 1 - (i - t.give)];
 }
 
-// Slots, positions, table and list entries, by `warps` warps of which this is `warp`. A warp
-// takes kPlanRows rows at a time: one search for the first, then sequences and pages are
-// followed.
+__device__ __forceinline__ void plan_row(const PlanArgs& a, int r, int pos, int page, int in_page) {
+  int slot = -1;
+  if (page >= 0 && page < a.n_pages)
+    slot = page * a.page_size + in_page;
+  else
+    set_status(a.hdr, ADASPARK_DEV_BAD_LAYOUT, 0x8200u);
+  a.slots[r] = slot;
+  a.positions[r] = pos;
+}
+
+// Slots, positions, table and list entries, by `warps` warps of which this is
+// `warp`. A page that is taken is written to its table by whoever has its first
+// token, which is always a new one.
 __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
                                            const PlanTotals& t, int warp, int warps) {
   const int lane = threadIdx.x & 31, rows = t.ok ? t.rows : 0;
-  for (int r0 = warp * kPlanRows; r0 < a.n_rows; r0 += warps * kPlanRows) {
-    int s = r0 < rows ? plan_find(p.starts, a.n_seqs, r0) : 0;
-    int seen = -1, seen_s = -1, page = 0;
-    for (int r = r0 + lane; r < min(r0 + kPlanRows, a.n_rows); r += 32) {
-      int slot = -1, pos = 0;
-      if (r < rows) {
-        while (s + 1 < a.n_seqs && p.starts[s + 1] <= r) ++s;
-        const int o = p.old_lens[s];
-        pos = o + r - p.starts[s];
-        const int col = pos / a.page_size;
-        if (col != seen || s != seen_s) {
-          const int held = plan_pages(o, a.page_size);
-          page = col < held ? a.table[s * a.table_stride + col]
-                            : plan_taken(a, p, t, p.take0[s] + col - held);
-          seen = col;
-          seen_s = s;
+  const int chunk = a.n_rows <= warps * 32 ? 32 : 128;
+  for (int r0 = warp * chunk; r0 < a.n_rows; r0 += warps * chunk) {
+    const int r1 = min(r0 + chunk, a.n_rows), r2 = min(r1, rows);
+    for (int r = max(r0, rows) + lane; r < r1; r += 32) {
+      a.slots[r] = -1;
+      a.positions[r] = 0;
+    }
+    if (r0 >= r2) continue;
+    int s = plan_find_warp(p.starts, a.n_seqs, r0);
+    if (plan_find_warp(p.starts, a.n_seqs, r2 - 1) - s < 8) {
+      // few sequences: the warp looks up 32 pages of one at a time
+      for (int ra = r0; ra < r2; ++s) {
+        const int st = p.starts[s], rb = s + 1 < a.n_seqs ? min(r2, p.starts[s + 1]) : r2;
+        const int o = p.old_lens[s], shift = o - st;  // position of row r: r + shift
+        const int held = plan_pages(a, o);
+        const int last = ra < rb ? plan_div(a, rb - 1 + shift) : -1;
+        for (int c0 = ra < rb ? plan_div(a, ra + shift) : 0; c0 <= last; c0 += 32) {
+          const int col = c0 + lane, taken = p.take0[s] - held;  // column c takes page taken + c
+          const int from = taken + max(c0, held);
+          const int giver = c0 + 31 >= held && from < t.give
+                                ? plan_find_warp(p.give0, a.n_seqs, from)
+                                : 0;
+          int page = -1;
+          if (col <= last && col < held) {
+            page = a.table[s * a.table_stride + col];
+          } else if (col <= last) {
+            page = plan_taken(a, p, t, taken + col, giver);
+            if (col * a.page_size - shift >= ra) a.table[s * a.table_stride + col] = page;
+          }
+          // rows of these pages; 64 bits: the last page's end may pass 2^31
+          const int rc = (int)min((long long)rb, (long long)(c0 + 32) * a.page_size - shift);
+          for (; ra < rc; ra += 32) {
+            const int r = min(ra + lane, rc - 1), pos = r + shift, c = plan_div(a, pos);
+            const int pg = __shfl_sync(0xffffffffu, page, c - c0);
+            if (ra + lane < rc) plan_row(a, r, pos, pg, pos - c * a.page_size);
+          }
+          ra = rc;
         }
-        if (page >= 0 && page < a.n_pages)
-          slot = page * a.page_size + pos - col * a.page_size;
-        else
-          set_status(a.hdr, ADASPARK_DEV_BAD_LAYOUT, 0x8200u);
       }
-      a.slots[r] = slot;
-      a.positions[r] = pos;
+    } else {
+      // many sequences: a lane looks up its own row
+      for (int r = r0 + lane; r < r2; r += 32) {
+        while (s + 1 < a.n_seqs && p.starts[s + 1] <= r) ++s;
+        const int o = p.old_lens[s], pos = o + r - p.starts[s], col = plan_div(a, pos);
+        const int held = plan_pages(a, o), i = p.take0[s] + col - held;
+        int page;
+        if (col < held) {
+          page = a.table[s * a.table_stride + col];
+        } else {
+          page = plan_taken(a, p, t, i, i < t.give ? plan_find(p.give0, a.n_seqs, i) : 0);
+          if (col * a.page_size == pos) a.table[s * a.table_stride + col] = page;
+        }
+        plan_row(a, r, pos, page, pos - col * a.page_size);
+      }
     }
   }
   if (!t.ok) return;
-  for (int i = warp * 32 + lane; i < t.take; i += warps * 32) {
-    const int s = plan_find(p.take0, a.n_seqs, i);
-    const int col = plan_pages(p.old_lens[s], a.page_size) + i - p.take0[s];
-    a.table[s * a.table_stride + col] = plan_taken(a, p, t, i);
-  }
   for (int g = t.take + warp * 32 + lane; g < t.give; g += warps * 32)
-    a.free_pages[t.n_free + t.give - 1 - g] = plan_given(a, p, g);
+    a.free_pages[t.n_free + t.give - 1 - g] =
+        plan_given(a, p, g, plan_find(p.give0, a.n_seqs, g));
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
@@ -228,13 +284,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs 
   if (threadIdx.x == 0) *plan_totals(a.hdr) = t;
 }
 
-__global__ void __launch_bounds__(256) plan_write_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_write_kernel(const PlanArgs a) {
   __shared__ PlanShared sh;
   dependency_release();
   dependency_wait();
   PlanSums p{a.old_lens, a.new_lens, a.take0, a.give0, a.starts};
   if (a.n_seqs <= kPlanSeqs) {
-    for (int i = threadIdx.x; i < a.n_seqs; i += 256) {
+    for (int i = threadIdx.x; i < a.n_seqs; i += kPlanThreads) {
       sh.old_lens[i] = a.old_lens[i];
       sh.new_lens[i] = a.new_lens[i];
       sh.take0[i] = a.take0[i];
@@ -244,7 +300,8 @@ __global__ void __launch_bounds__(256) plan_write_kernel(const PlanArgs a) {
     __syncthreads();
     p = {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts};
   }
-  plan_write(a, p, *plan_totals(a.hdr), blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
+  constexpr int W = kPlanThreads / 32;
+  plan_write(a, p, *plan_totals(a.hdr), blockIdx.x * W + (threadIdx.x >> 5), gridDim.x * W);
 }
 
 }  // namespace adaspark
@@ -291,15 +348,21 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   a.starts = token_starts; a.slots = slots; a.positions = positions;
   a.n_seqs = n_seqs; a.max_pages = max_pages; a.page_size = page_size;
   a.n_pages = n_pages; a.n_rows = n_rows;
+  // with 2^(k-1) < page_size <= 2^k, ceil(2^(31+k) / page_size) < 2^32 divides every n < 2^31
+  int k = 0;
+  while ((int64_t)1 << k < page_size) ++k;
+  a.div_shift = 31 + k;
+  a.div_mul = (uint32_t)((((uint64_t)1 << (31 + k)) + page_size - 1) / page_size);
   if (n_rows <= kPlanOneBlock && n_seqs <= kPlanSeqs)
     return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a));
   cudaError_t e =
       launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
   if (e == cudaSuccess) {
-    const int64_t want = ((int64_t)n_rows + 8 * kPlanRows - 1) / (8 * kPlanRows);
-    const int64_t most = (int64_t)sms * 8;
+    const int64_t want = ((int64_t)n_rows + 4095) / 4096;  // 128 rows a warp
+    const int64_t most = (int64_t)sms * 2;
     const unsigned grid = (unsigned)(want < most ? want : most);
-    e = launch_after("kv_plan_write", plan_write_kernel, dim3(grid), dim3(256), 0, s, a);
+    e = launch_after("kv_plan_write", plan_write_kernel, dim3(grid), dim3(kPlanThreads), 0,
+                     s, a);
   }
   return cuda_status(e);
 }
