@@ -111,6 +111,8 @@ def lib():
             "adaspark_layer_buffers": (i32, [i32] * 9 + [ctypes.POINTER(ctypes.c_size_t)]),
             "adaspark_layer": (i32, [vp] * 8 + [i32, vp, vp, vp] + [i32] * 8 +
                                [f32, f32, vp, vp, sz, vp]),
+            "adaspark_layer_rope": (i32, [vp] * 8 + [i32, vp, vp, vp] + [i32] * 8 + [f32, f32] +
+                                    rope + [vp, vp, sz, vp]),
             "adaspark_rmsnorm": (i32, [vp, i32, vp, vp, i32, i32, f32, vp]),
             "adaspark_rope_frequencies": (i32, [i32, f64, i32, f64, i32, ctypes.POINTER(f64),
                                                 ctypes.POINTER(f32)]),
@@ -456,9 +458,12 @@ def layer_workspace_bytes(n_tokens, n_vis, n_cubes, hq, hkv, d, D, F, dtype=BF16
 
 
 def layer(x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down, cube_ids, cube_offsets, text_mask, n_vis,
-          hq, hkv, p_attn, p_ffn, y=None, workspace=None, stream=None):
+          hq, hkv, p_attn, p_ffn, y=None, workspace=None, stream=None, positions=None, freq=None,
+          w_qnorm=None, w_knorm=None, eps=1e-6, interleaved=False, sections=None, magnitude=1.0):
     """A whole AdaSpark layer (projections, AdaS-Attn, output projection with the
-    residual, AdaS-FFN); weights in [out, in] layout. Returns (y fp32, workspace)."""
+    residual, AdaS-FFN); weights in [out, in] layout. Returns (y fp32, workspace).
+    With ``freq`` (rotary positions) or ``w_qnorm`` / ``w_knorm`` (per-head norms)
+    queries and keys go through qk_rope before the attention."""
     import torch
     for t, nm in ((x, "x"), (W_q, "W_q"), (W_k, "W_k"), (W_v, "W_v"), (W_o, "W_o"),
                   (W_gate, "W_gate"), (W_up, "W_up"), (W_down, "W_down"),
@@ -477,6 +482,31 @@ def layer(x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down, cube_ids, cube_offsets, t
         if nb == 0:
             raise AdasparkError(EINVAL, "adaspark_layer_workspace")
         workspace = torch.empty(nb, dtype=torch.uint8, device=x.device)
+    if freq is not None or w_qnorm is not None or w_knorm is not None:
+        for t, nm, ty, shape in (
+                (freq, "freq", torch.float64, None), (w_qnorm, "w_qnorm", x.dtype, (d,)),
+                (w_knorm, "w_knorm", x.dtype, (d,)),
+                (positions if freq is not None else None, "positions", torch.int32,
+                 (N,) if sections is None else (3, N))):
+            if t is not None:
+                _need(t, nm)
+                if t.dtype != ty or (shape is not None and tuple(t.shape) != shape):
+                    raise ValueError(f"{nm} must be {ty} {shape or ''}, got {t.dtype} "
+                                     f"{tuple(t.shape)}")
+        if freq is not None and positions is None:
+            raise ValueError("positions is required")
+        if sections is not None and len(sections) != 3:
+            raise ValueError("sections must be three numbers of pairs")
+        _check(lib().adaspark_layer_rope(
+            _ptr(x), _ptr(W_q), _ptr(W_k), _ptr(W_v), _ptr(W_o), _ptr(W_gate), _ptr(W_up),
+            _ptr(W_down), dt, _ptr(cube_ids), _ptr(cube_offsets), _ptr(text_mask), C, n_vis, N, hq,
+            hkv, d, D, F, float(p_attn), float(p_ffn), _ptr(positions),
+            1 if sections is None else 3,
+            None if sections is None else (ctypes.c_int32 * 3)(*sections), _ptr(freq),
+            0 if freq is None else 2 * freq.numel(), 1 if interleaved else 0, float(magnitude),
+            _ptr(w_qnorm), _ptr(w_knorm), float(eps), _ptr(y), _ptr(workspace), workspace.numel(),
+            _stream(stream)), "adaspark_layer_rope")
+        return y, workspace
     _check(lib().adaspark_layer(_ptr(x), _ptr(W_q), _ptr(W_k), _ptr(W_v), _ptr(W_o),
                                 _ptr(W_gate), _ptr(W_up), _ptr(W_down), dt, _ptr(cube_ids),
                                 _ptr(cube_offsets), _ptr(text_mask), C, n_vis, N, hq, hkv, d, D, F,

@@ -1,5 +1,6 @@
 // A whole AdaSpark layer as the stacked configuration wires it, and RMSNorm:
 //   Q = x W_q^T, K = x W_k^T, V = x W_v^T        (tcgen05 GEMMs, bf16 out)
+//   [Q, K = per-head norm and rotary positions   (adaspark_qk_rope, in place)]
 //   a = AdaS-Attn(Q, K, V; p_attn)               (adaspark_cube_attn)
 //   h = x + a W_o^T                              (tcgen05 GEMM, residual epilogue)
 //   y = AdaS-FFN(h; p_ffn)                       (adaspark_token_ffn, fp32 out)
@@ -10,6 +11,7 @@
 
 #include "attn_kernels.h"
 #include "ffn_kernels.h"
+#include "serve.h"
 
 using namespace adaspark;
 
@@ -98,6 +100,86 @@ int cuda_rc(cudaError_t e) { return e == cudaSuccess ? ADASPARK_OK : ADASPARK_EC
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Per-head norms and rotary positions between the projections and the attention.
+struct LayerRope {
+  const int32_t* positions;
+  int n_axes;
+  const int32_t* sections;
+  const double* freq;
+  int rot, interleaved;
+  float magnitude;
+  const void *w_q, *w_k;
+  float eps;
+};
+
+int qk_rope_call(const LayerRope* r, __nv_bfloat16* Q, __nv_bfloat16* K, int n_tokens, int hq,
+                 int hkv, int d, void* stream) {
+  return adaspark_qk_rope(Q, (int64_t)hq * d, d, K, (int64_t)hkv * d, d, ADASPARK_BF16,
+                          r->positions, r->n_axes, r->sections, r->freq, r->rot, r->interleaved,
+                          r->magnitude, r->w_q, r->w_k, r->eps, n_tokens, hq, hkv, d, Q,
+                          (int64_t)hq * d, d, K, (int64_t)hkv * d, d, stream);
+}
+
+int run_layer(const void* x, const void* W_q, const void* W_k, const void* W_v,
+              const void* W_o, const void* W_gate, const void* W_up, const void* W_down, int dtype,
+              const int32_t* cube_ids, const int32_t* cube_offsets, const uint8_t* text_mask,
+              int n_cubes, int n_vis, int n_tokens, int hq, int hkv, int d, int D, int F,
+              float p_attn, float p_ffn, float* y,
+              void* workspace, size_t workspace_bytes, void* stream, const LayerRope* rope) {
+  if (!x || !W_q || !W_k || !W_v || !W_o || !W_gate || !W_up || !W_down || !cube_ids ||
+      !cube_offsets || !text_mask || !y || !workspace)
+    return ADASPARK_EINVAL;
+  if (dtype == ADASPARK_FP32) return ADASPARK_EUNSUPPORTED;
+  if (dtype != ADASPARK_BF16 || !layer_sizes_ok(n_tokens, n_vis, n_cubes, hq, hkv, d, D, F))
+    return ADASPARK_EINVAL;
+  if (!(p_attn > 0.f && p_attn <= 1.f) || !(p_ffn > 0.f && p_ffn <= 1.f)) return ADASPARK_EINVAL;
+  LayerLayout L{};
+  if (!layer_layout(n_tokens, n_vis, n_cubes, hq, hkv, d, D, F, &L)) return ADASPARK_EINVAL;
+  if (workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & (kLayerAlign - 1)))
+    return ADASPARK_EINVAL;
+  for (const void* ptr : {x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down,
+                          static_cast<const void*>(y)})
+    if (!aligned16(ptr)) return ADASPARK_EINVAL;
+
+  if (rope && !qk_rope_args_ok(rope->freq, rope->rot, d, rope->positions, rope->n_axes,
+                               rope->sections, rope->magnitude, rope->w_q, rope->w_k, rope->eps))
+    return ADASPARK_EINVAL;
+
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  WsHeader* hdr = reinterpret_cast<WsHeader*>(ws + L.header);
+  auto* Q = reinterpret_cast<__nv_bfloat16*>(ws + L.q);
+  auto* K = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
+  auto* V = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
+  auto* A = reinterpret_cast<__nv_bfloat16*>(ws + L.a);
+  auto* H = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
+  const auto* X = static_cast<const __nv_bfloat16*>(x);
+  if (cudaMemsetAsync(hdr, 0, sizeof(WsHeader), s) != cudaSuccess) return ADASPARK_ECUDA;
+  int rc;
+  if ((rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_q), nullptr, Q,
+                                     n_tokens, hq * d, D, hdr, s))) ||
+      (rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_k), nullptr, K,
+                                     n_tokens, hkv * d, D, hdr, s))) ||
+      (rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_v), nullptr, V,
+                                     n_tokens, hkv * d, D, hdr, s))))
+    return rc;
+  if (rope && (rc = qk_rope_call(rope, Q, K, n_tokens, hq, hkv, d, stream))) return rc;
+  if ((rc = adaspark_cube_attn(Q, K, V, ADASPARK_BF16, cube_ids, cube_offsets, n_cubes, n_vis,
+                               n_tokens, hq, hkv, d, p_attn, A, ws + L.attn_ws, L.attn_bytes,
+                               stream)))
+    return rc;
+  if ((rc = cuda_rc(launch_linear_tc(A, static_cast<const __nv_bfloat16*>(W_o), X, H, n_tokens,
+                                     D, hq * d, hdr, s))))
+    return rc;
+  if ((rc = adaspark_token_ffn(H, W_gate, W_up, W_down, ADASPARK_BF16, cube_ids, cube_offsets,
+                               text_mask, n_cubes, n_vis, n_tokens, D, F, p_ffn, y,
+                               ws + L.ffn_ws, L.ffn_bytes, stream)))
+    return rc;
+  return cuda_rc(launch("merge_status", merge_status_kernel, dim3(1), dim3(1), 0, s, hdr,
+                        reinterpret_cast<const WsHeader*>(ws + L.attn_ws),
+                        reinterpret_cast<const WsHeader*>(ws + L.ffn_ws)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,53 +215,25 @@ int adaspark_layer(const void* x, const void* W_q, const void* W_k, const void* 
                    const uint8_t* text_mask, int n_cubes, int n_vis, int n_tokens, int hq,
                    int hkv, int d, int D, int F, float p_attn, float p_ffn, float* y,
                    void* workspace, size_t workspace_bytes, void* stream) {
-  if (!x || !W_q || !W_k || !W_v || !W_o || !W_gate || !W_up || !W_down || !cube_ids ||
-      !cube_offsets || !text_mask || !y || !workspace)
-    return ADASPARK_EINVAL;
-  if (dtype == ADASPARK_FP32) return ADASPARK_EUNSUPPORTED;
-  if (dtype != ADASPARK_BF16 || !layer_sizes_ok(n_tokens, n_vis, n_cubes, hq, hkv, d, D, F))
-    return ADASPARK_EINVAL;
-  if (!(p_attn > 0.f && p_attn <= 1.f) || !(p_ffn > 0.f && p_ffn <= 1.f)) return ADASPARK_EINVAL;
-  LayerLayout L{};
-  if (!layer_layout(n_tokens, n_vis, n_cubes, hq, hkv, d, D, F, &L)) return ADASPARK_EINVAL;
-  if (workspace_bytes < L.total || (reinterpret_cast<uintptr_t>(workspace) & (kLayerAlign - 1)))
-    return ADASPARK_EINVAL;
-  for (const void* ptr : {x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down,
-                          static_cast<const void*>(y)})
-    if (!aligned16(ptr)) return ADASPARK_EINVAL;
+  return run_layer(x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down, dtype, cube_ids, cube_offsets,
+                   text_mask, n_cubes, n_vis, n_tokens, hq, hkv, d, D, F, p_attn, p_ffn, y,
+                   workspace, workspace_bytes, stream, nullptr);
+}
 
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  WsHeader* hdr = reinterpret_cast<WsHeader*>(ws + L.header);
-  auto* Q = reinterpret_cast<__nv_bfloat16*>(ws + L.q);
-  auto* K = reinterpret_cast<__nv_bfloat16*>(ws + L.k);
-  auto* V = reinterpret_cast<__nv_bfloat16*>(ws + L.v);
-  auto* A = reinterpret_cast<__nv_bfloat16*>(ws + L.a);
-  auto* H = reinterpret_cast<__nv_bfloat16*>(ws + L.h);
-  const auto* X = static_cast<const __nv_bfloat16*>(x);
-  if (cudaMemsetAsync(hdr, 0, sizeof(WsHeader), s) != cudaSuccess) return ADASPARK_ECUDA;
-  int rc;
-  if ((rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_q), nullptr, Q,
-                                     n_tokens, hq * d, D, hdr, s))) ||
-      (rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_k), nullptr, K,
-                                     n_tokens, hkv * d, D, hdr, s))) ||
-      (rc = cuda_rc(launch_linear_tc(X, static_cast<const __nv_bfloat16*>(W_v), nullptr, V,
-                                     n_tokens, hkv * d, D, hdr, s))))
-    return rc;
-  if ((rc = adaspark_cube_attn(Q, K, V, ADASPARK_BF16, cube_ids, cube_offsets, n_cubes, n_vis,
-                               n_tokens, hq, hkv, d, p_attn, A, ws + L.attn_ws, L.attn_bytes,
-                               stream)))
-    return rc;
-  if ((rc = cuda_rc(launch_linear_tc(A, static_cast<const __nv_bfloat16*>(W_o), X, H, n_tokens,
-                                     D, hq * d, hdr, s))))
-    return rc;
-  if ((rc = adaspark_token_ffn(H, W_gate, W_up, W_down, ADASPARK_BF16, cube_ids, cube_offsets,
-                               text_mask, n_cubes, n_vis, n_tokens, D, F, p_ffn, y,
-                               ws + L.ffn_ws, L.ffn_bytes, stream)))
-    return rc;
-  return cuda_rc(launch("merge_status", merge_status_kernel, dim3(1), dim3(1), 0, s, hdr,
-                        reinterpret_cast<const WsHeader*>(ws + L.attn_ws),
-                        reinterpret_cast<const WsHeader*>(ws + L.ffn_ws)));
+int adaspark_layer_rope(const void* x, const void* W_q, const void* W_k, const void* W_v,
+                        const void* W_o, const void* W_gate, const void* W_up, const void* W_down,
+                        int dtype, const int32_t* cube_ids, const int32_t* cube_offsets,
+                        const uint8_t* text_mask, int n_cubes, int n_vis, int n_tokens, int hq,
+                        int hkv, int d, int D, int F, float p_attn, float p_ffn,
+                        const int32_t* positions, int n_axes, const int32_t* sections,
+                        const double* freq, int rot, int interleaved, float magnitude,
+                        const void* w_q, const void* w_k, float eps, float* y, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const LayerRope rope{positions, n_axes, sections, freq, rot, interleaved, magnitude, w_q, w_k,
+                       eps};
+  return run_layer(x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down, dtype, cube_ids, cube_offsets,
+                   text_mask, n_cubes, n_vis, n_tokens, hq, hkv, d, D, F, p_attn, p_ffn, y,
+                   workspace, workspace_bytes, stream, &rope);
 }
 
 int adaspark_rmsnorm(const void* x, int x_dtype, const void* weight, void* out, int n_rows,

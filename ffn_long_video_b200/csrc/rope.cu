@@ -436,13 +436,10 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-namespace {
-
-constexpr int kBwdMaxBlocks = 148 * kBwdBlocksPerSm;
-
-// The arguments that describe positions and rotation.
-bool rope_ok(const double* freq, int rot, int d, const int32_t* positions, int n_axes,
-             const int32_t* sections, float magnitude) {
+bool qk_rope_args_ok(const double* freq, int rot, int d, const int32_t* positions, int n_axes,
+                     const int32_t* sections, float magnitude, const void* w_q, const void* w_k,
+                     float eps) {
+  if (!(eps >= 0.f) || !aligned(w_q, 16) || !aligned(w_k, 16)) return false;
   if (rot < 0 || rot > d || rot % 16 != 0) return false;
   if (rot == 0) return true;
   if (!freq || !positions || !aligned(freq, 8) || !aligned(positions, 4)) return false;
@@ -456,6 +453,10 @@ bool rope_ok(const double* freq, int rot, int d, const int32_t* positions, int n
   }
   return sum == rot / 2;
 }
+
+namespace {
+
+constexpr int kBwdMaxBlocks = 148 * kBwdBlocksPerSm;
 
 void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions, int n_axes,
               const int32_t* sections, float magnitude, int n) {
@@ -583,10 +584,10 @@ int adaspark_qk_rope(const void* Q, int64_t q_ts, int64_t q_hs, const void* K, i
     return ADASPARK_EINVAL;
   if (n_tokens == 0) return ADASPARK_OK;
   if (!Q || !K || !Q_out || !K_out) return ADASPARK_EINVAL;
-  if (!rope_ok(freq, rot, d, positions, n_axes, sections, magnitude)) return ADASPARK_EINVAL;
+  if (!qk_rope_args_ok(freq, rot, d, positions, n_axes, sections, magnitude, w_q, w_k, eps))
+    return ADASPARK_EINVAL;
   if (!rows_aligned(Q, q_ts, q_hs, dtype) || !rows_aligned(K, k_ts, k_hs, dtype) ||
-      !rows_aligned(Q_out, qo_ts, qo_hs, dtype) || !rows_aligned(K_out, ko_ts, ko_hs, dtype) ||
-      !aligned(w_q, 16) || !aligned(w_k, 16))
+      !rows_aligned(Q_out, qo_ts, qo_hs, dtype) || !rows_aligned(K_out, ko_ts, ko_hs, dtype))
     return ADASPARK_EINVAL;
   if (!rows_distinct(n_tokens, hq, d, qo_ts, qo_hs) || !rows_distinct(n_tokens, hkv, d, ko_ts, ko_hs))
     return ADASPARK_EINVAL;
@@ -614,12 +615,13 @@ int adaspark_qk_rope_append(const void* Q, int64_t q_ts, int64_t q_hs, const voi
     return ADASPARK_EINVAL;
   if (n_tokens == 0) return ADASPARK_OK;
   if (!Q || !K || !V || !Q_out || !slots) return ADASPARK_EINVAL;
-  if (!rope_ok(freq, rot, d, positions, n_axes, sections, magnitude)) return ADASPARK_EINVAL;
+  if (!qk_rope_args_ok(freq, rot, d, positions, n_axes, sections, magnitude, w_q, w_k, eps))
+    return ADASPARK_EINVAL;
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
   if (!cache_ok(k_cache, v_cache, cs, hkv, d, dtype)) return ADASPARK_EINVAL;
   if (!rows_aligned(Q, q_ts, q_hs, dtype) || !rows_aligned(K, k_ts, k_hs, dtype) ||
       !rows_aligned(V, v_ts, v_hs, dtype) || !rows_aligned(Q_out, qo_ts, qo_hs, dtype) ||
-      !aligned(w_q, 16) || !aligned(w_k, 16) || !aligned(slots, 4))
+      !aligned(slots, 4))
     return ADASPARK_EINVAL;
   if (!rows_distinct(n_tokens, hq, d, qo_ts, qo_hs)) return ADASPARK_EINVAL;
   int sms = 0;
@@ -689,11 +691,11 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     return ADASPARK_OK;
   }
   if (!dQ_out || !dK_out || !dQ || !dK) return ADASPARK_EINVAL;
-  if (!rope_ok(freq, rot, d, positions, n_axes, sections, magnitude)) return ADASPARK_EINVAL;
+  if (!qk_rope_args_ok(freq, rot, d, positions, n_axes, sections, magnitude, w_q, w_k, eps))
+    return ADASPARK_EINVAL;
   if ((w_q && !Q) || (w_k && !K)) return ADASPARK_EINVAL;
   if (!rows_aligned(dQ_out, dq_ts, dq_hs, dy_dtype) ||
-      !rows_aligned(dK_out, dk_ts, dk_hs, dy_dtype) || !aligned(dQ, 16) || !aligned(dK, 16) ||
-      !aligned(w_q, 16) || !aligned(w_k, 16))
+      !rows_aligned(dK_out, dk_ts, dk_hs, dy_dtype) || !aligned(dQ, 16) || !aligned(dK, 16))
     return ADASPARK_EINVAL;
   if ((w_q && !rows_aligned(Q, q_ts, q_hs, dtype)) ||
       (w_k && !rows_aligned(K, k_ts, k_hs, dtype)))

@@ -52,6 +52,11 @@ inline bool cache_ok(const void* k, const void* v, const CacheRows& c, int hkv, 
   return c.n_pages == 1 || c.ps >= page_span;
 }
 
+// The arguments that describe norm, positions and rotation (rope.cu).
+bool qk_rope_args_ok(const double* freq, int rot, int d, const int32_t* positions, int n_axes,
+                     const int32_t* sections, float magnitude, const void* w_q, const void* w_k,
+                     float eps);
+
 inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? ADASPARK_OK : ADASPARK_ECUDA; }
 
 // V (4 or 8) consecutive elements as they lie in memory, and as fp32 pairs.

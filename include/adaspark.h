@@ -449,6 +449,20 @@ int adaspark_layer(const void *x, const void *W_q, const void *W_k, const void *
                    int hkv, int d, int D, int F, float p_attn, float p_ffn, float *y,
                    void *workspace, size_t workspace_bytes, void *stream);
 
+/* adaspark_layer with per-head norms and rotary positions of Q and K between the
+ * projections and AdaS-Attn (adaspark_qk_rope in place, whose arguments these
+ * are; the layer's Q and K buffers then hold the rotated rows). Everything else,
+ * workspace and buffers included, as for adaspark_layer. */
+int adaspark_layer_rope(const void *x, const void *W_q, const void *W_k, const void *W_v,
+                        const void *W_o, const void *W_gate, const void *W_up, const void *W_down,
+                        int dtype, const int32_t *cube_ids, const int32_t *cube_offsets,
+                        const uint8_t *text_mask, int n_cubes, int n_vis, int n_tokens, int hq,
+                        int hkv, int d, int D, int F, float p_attn, float p_ffn,
+                        const int32_t *positions, int n_axes, const int32_t *sections,
+                        const double *freq, int rot, int interleaved, float magnitude,
+                        const void *w_q, const void *w_k, float eps, float *y, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 /* Byte offsets inside an adaspark_layer workspace of the layer's intermediate
  * tensors after a call: offsets[0..6] = Q, K, V, a (attention output), h, the
  * AdaS-Attn workspace and the AdaS-FFN workspace (for their export and stats

@@ -248,6 +248,19 @@ def test_decode_attn_refusals(change):
     assert _call("decode_attn", DECODE_ORDER, base, change) == fb.EINVAL
 
 
+@pytest.mark.parametrize("change", [dict(pos=None), dict(freq=None), dict(rot=8), dict(axes=2),
+                                    dict(sec=BAD_SEC), dict(sec=None), dict(eps=-1.0),
+                                    dict(mag=float("nan")), dict(wq=ODD), dict(x=None),
+                                    dict(ws=None), dict(wsb=8)])
+def test_layer_rope_refusals(change):
+    base = dict(ROPE, x=P, Wq=P, Wk=P, Wv=P, Wo=P, Wg=P, Wu=P, Wd=P, ids=P, off=P, text=P, C=16,
+                nv=512, n=544, hq=4, hkv=1, D=256, F=512, pa=0.7, pf=0.7, y=P, ws=P,
+                wsb=fb.layer_workspace_bytes(544, 512, 16, 4, 1, 128, 256, 512))
+    order = ("x Wq Wk Wv Wo Wg Wu Wd dtype ids off text C nv n hq hkv d D F pa pf pos axes sec freq "
+             "rot il mag wq wk eps y ws wsb stream")
+    assert _call("layer_rope", order, base, change) == fb.EINVAL
+
+
 def test_workspace_queries_of_bad_sizes_are_zero():
     assert fb.kv_plan_workspace_bytes(0) == 0
     assert fb.qk_rope_backward_workspace_bytes(-1, 8, 2, 128) == 0

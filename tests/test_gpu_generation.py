@@ -120,3 +120,42 @@ def test_decoding_continues_the_prompt(name, graph):
                                full(t["V"], n).cpu().float().numpy(), np.zeros((1, 1), int), [n])
         assert np.abs(lse[s].double().cpu().numpy() - l[0]).max() <= 1e-4
         assert np.abs(out[s].double().cpu().numpy() - o[0]).max() <= (2e-2 if dt == fb.BF16 else 1e-4)
+
+
+@pytest.mark.parametrize("rotate,norm", [(True, True), (True, False), (False, True)])
+def test_layer_with_positions(rotate, norm):
+    """The layer's own path through qk_rope: its Q and K are the rotated
+    projections and its attention the standalone call's, bit for bit."""
+    cfg = workloads.small_config(name="gen-layer", grid=(4, 8, 8), cube=(4, 4, 4), n_text=23, D=256,
+                                 hq=6, hkv=3, F=256, seed=73)
+    t = {k: v.cuda() for k, v in workloads.make_stack(cfg, 0).items()}
+    W = [t[k].t().contiguous() for k in ("W_q", "W_k", "W_v", "W_o")]
+    ids, off, text, _ = parity.layout_tensors(cfg, "cuda")
+    args = (t["x"], *W, t["W_gate"], t["W_up"], t["W_down"], ids, off, text, cfg.n_vis, cfg.hq,
+            cfg.hkv, 0.7, 0.7)
+    sizes = (cfg.n_tokens, cfg.n_vis, cfg.n_cubes, cfg.hq, cfg.hkv, cfg.d, cfg.D, cfg.F)
+    _, ws = fb.layer(*args)
+    plain = {k: v.clone() for k, v in fb.layer_buffers(ws, *sizes).items() if k in "QKV"}
+    kw = {}
+    g = torch.Generator().manual_seed(4)
+    pos = torch.from_numpy(video_positions(cfg)).cuda()
+    freq = torch.from_numpy(fb.rope_frequencies(cfg.d, 1e6)[0]).cuda()
+    w = (1 + 0.2 * torch.randn(2, cfg.d, generator=g)).to(torch.bfloat16).cuda()
+    if rotate:
+        kw.update(positions=pos, freq=freq, sections=(16, 24, 24), magnitude=1.1)
+    if norm:
+        kw.update(w_qnorm=w[0].contiguous(), w_knorm=w[1].contiguous())
+    y, ws = fb.layer(*args, **kw)
+    assert fb.read_device_status(ws)[0] == fb.OK
+    buf = fb.layer_buffers(ws, *sizes)
+    Q, K = fb.qk_rope(plain["Q"], plain["K"], kw.get("positions"), kw.get("freq"),
+                      w_q=kw.get("w_qnorm"), w_k=kw.get("w_knorm"), sections=kw.get("sections"),
+                      magnitude=kw.get("magnitude", 1.0))
+    assert torch.equal(buf["Q"], Q) and torch.equal(buf["K"], K)
+    assert torch.equal(buf["V"], plain["V"])
+    out, _ = fb.cube_attn(Q, K, plain["V"], ids, off, cfg.n_vis, 0.7)
+    assert torch.equal(buf["a"], out) and torch.isfinite(y).all()
+    with pytest.raises(ValueError):
+        fb.layer(*args, freq=freq)
+    with pytest.raises(fb.AdasparkError):
+        fb.layer(*args, freq=freq, positions=pos, sections=(16, 24, 23))
