@@ -34,22 +34,26 @@ struct RopeArgs {
   void *kc, *vc;
   CacheRows cs;
   int32_t rot, sec0, sec01;      // pairs below sec0 use axis 0, below sec01 axis 1, others 2
-  int32_t n, hq, hkv, parts;
+  int32_t n, hq, hkv;
   float eps, magnitude;
 };
 
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
-// Forward: runs of 8 elements and blocks that stay, 7 of them on an SM for bf16
-// (70 registers). 65792 tokens of 28 + 4 heads of 128, with the caches read cold:
-// 163 us at 7, 177 at 8 (spills), 190 for blocks that end after a token; runs of
-// 4 elements 212. 18559 normalised tokens of 16 + 2 heads: 34, 36, 38 and 42 us.
+// Forward: runs of 8 elements, 7 blocks on an SM for bf16 (72 registers). 65792
+// tokens of 28 + 4 heads of 128: 162 us at 7, 169 at 6, 181 at 5, 171 at 9
+// (spills); 18559 normalised tokens of 16 + 2 heads: 28, 31, 33 and 29 us (the
+// floors at 6.46 TB/s: 167 and 26.5 us). Before that, with one loop over queries
+// and keys that selects its pointers a step: 163 and 34 us; with blocks that end
+// after a token: 190 and 42 us.
 constexpr int kRopeRun = 8;
 template <typename T>
 constexpr int kRopeBlocks = sizeof(T) == 2 ? 7 : 5;
-// Backward: 5 blocks per SM. 18560 tokens of 16 + 2 normalised heads: 73 us at 5,
-// 79 at 4, 98 at 6 and 113 at 8 (spills); 154 before the next step's rows were
-// loaded ahead.
+// Backward: runs of 4 elements (half the values per lane beside 32 sums for the
+// weights), 5 blocks on an SM. 18560 tokens of 16 + 2 normalised heads: 73 us at 5
+// (floor 66), 77 at 4 and at 6; runs of 8 at 3 blocks 73; 154 us before the next
+// step's rows were loaded ahead.
+constexpr int kBwdRun = 4;
 constexpr int kBwdBlocksPerSm = 5;
 
 // A head's lanes, each with two runs of V elements.
@@ -81,35 +85,60 @@ __device__ __forceinline__ int rope_pair(int l, int e, int rot) {
   return e < V / 2 ? V / 2 * l + e : V / 2 * l + (rot >> 2) + (e - V / 2);
 }
 
-// The rotation of one token for this lane's V pairs, as factors of element pairs.
-// The lanes of the warp that stand at the same place of different heads share
-// their angles: each computes V / heads of them and the warp exchanges them.
-// Lanes outside the rotated part hold the identity. BACK: the transpose.
+// The pairs whose angles this lane computes. The lanes of the warp that stand at
+// the same place of different heads share their angles: each computes V / heads
+// of them and the warp exchanges them.
 template <int D, bool IL, int V>
+struct RopePairs {
+  using M = RopeMap<D, V>;
+  double freq[M::kAngles];   // in turns per position; 0 outside the rotated part
+  int64_t axis[M::kAngles];  // offset of the pair's axis of positions
+
+  __device__ __forceinline__ RopePairs(const RopeArgs& a, int lane) {
+    const int l = lane % M::kLanes, grp = lane / M::kLanes;
+#pragma unroll
+    for (int i = 0; i < M::kAngles; ++i) {
+      freq[i] = 0.0;
+      axis[i] = 0;
+      if (l < a.rot / (2 * V)) {
+        const int pair = rope_pair<IL, V>(l, grp * M::kAngles + i, a.rot);
+        freq[i] = a.freq[pair] * kInvTwoPi;
+        axis[i] = (pair < a.sec0 ? 0 : pair < a.sec01 ? 1 : 2) * a.pos_axis;
+      }
+    }
+  }
+  __device__ __forceinline__ void positions(const RopeArgs& a, int t, int (&p)[M::kAngles]) const {
+#pragma unroll
+    for (int i = 0; i < M::kAngles; ++i) p[i] = a.rot > 0 ? a.pos[axis[i] + t] : 0;
+  }
+};
+
+// The rotation of one token for this lane's V pairs, as factors of element pairs;
+// lanes outside the rotated part leave their elements alone. FULL: there are none
+// (known at compile time, 18559 normalised tokens take 28 us instead of 30).
+// BACK: the transpose.
+template <int D, bool IL, int V, bool FULL = false>
 struct RopeTurn {
   using M = RopeMap<D, V>;
   // halves: c, s, -s of elements (2i, 2i + 1); interleaved: (c, c) and (-s, s) of pair i
   F2 c[IL ? V : V / 2], s[IL ? V : V / 2], ns[IL ? 1 : V / 2];
+  bool turns;
 
   template <bool BACK>
-  __device__ __forceinline__ void set(const RopeArgs& a, int t, int lane) {
-    const int l = lane % M::kLanes, grp = lane / M::kLanes;
+  __device__ __forceinline__ void set(const RopeArgs& a, const RopePairs<D, IL, V>& pairs,
+                                      const int (&p)[M::kAngles], int lane) {
+    const int l = lane % M::kLanes;
     float mc[M::kAngles], ms[M::kAngles];
 #pragma unroll
     for (int i = 0; i < M::kAngles; ++i) {
-      mc[i] = 1.f;
-      ms[i] = 0.f;
-      if (l < a.rot / (2 * V)) {
-        const int pair = rope_pair<IL, V>(l, grp * M::kAngles + i, a.rot);
-        const int axis = pair < a.sec0 ? 0 : pair < a.sec01 ? 1 : 2;
-        const double turn = (double)a.pos[axis * a.pos_axis + t] * a.freq[pair] * kInvTwoPi;
-        float sn, cn;
-        sincospif(2.f * (float)(turn - rint(turn)), &sn, &cn);
-        mc[i] = cn * a.magnitude;
-        ms[i] = (BACK ? -sn : sn) * a.magnitude;
-      }
+      const double turn = (double)p[i] * pairs.freq[i];
+      float sn, cn;
+      sincospif(2.f * (float)(turn - rint(turn)), &sn, &cn);
+      mc[i] = cn * a.magnitude;
+      ms[i] = (BACK ? -sn : sn) * a.magnitude;
     }
     float ce[V], se[V];
+    turns = l < a.rot / (2 * V);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const int src = (e / M::kAngles) * M::kLanes + l;
@@ -134,6 +163,7 @@ struct RopeTurn {
 
   // Rotates a lane's two runs in place.
   __device__ __forceinline__ void turn(F2 (&u)[V / 2], F2 (&v)[V / 2]) const {
+    if (!FULL && !turns) return;
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       if (IL) {
@@ -175,222 +205,331 @@ __device__ __forceinline__ void load_f2(const float* p, F2 (&v)[V / 2]) {
     v[2 * i + 1] = f2(x.z, x.w);
   }
 }
+// Sum of the squares of a head's elements.
+template <int V, int LANES>
+__device__ __forceinline__ float head_squares(const F2 (&u)[V / 2], const F2 (&v)[V / 2]) {
+  F2 ss = mul2(u[0], u[0]);
+#pragma unroll
+  for (int i = 1; i < V / 2; ++i) ss = fma2(u[i], u[i], ss);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) ss = fma2(v[i], v[i], ss);
+  const float2 two = unpack(ss);
+  return head_sum<LANES>(two.x + two.y);
+}
 
-// Warps walk items (token, part of its heads): queries, then keys, then (with a
-// cache) values, which are copied. The next step's rows, of the next item too,
-// are on their way while a step is computed.
-template <typename T, int D, bool IL, bool CACHE, bool NORM>
-__global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_kernel(const RopeArgs a) {
+// A lane's two runs of a row, as they lie in memory; `gap`: elements between them.
+template <typename T, int V>
+struct RopeRow {
+  Raw<T, V> u, v;
+  __device__ __forceinline__ void load(const T* p, int gap) {
+    u.load(p);
+    v.load(p + gap);
+  }
+  __device__ __forceinline__ void store(T* p, int gap) const {
+    u.store(p);
+    v.store(p + gap);
+  }
+};
+
+// Norm and rotation of a row.
+template <typename T, int D, bool IL, bool NORM, int V, bool FULL>
+__device__ __forceinline__ void rope_head(RopeRow<T, V>& row,
+                                          const RopeTurn<D, IL, V, FULL>& rotation, const float* w, bool has_w, int e0, int gap, float eps) {
+  F2 u[V / 2], v[V / 2];
+  row.u.get(u);
+  row.v.get(v);
+  if constexpr (NORM) {
+    const float sum = head_squares<V, RopeMap<D, V>::kLanes>(u, v);
+    const float r = has_w ? rsqrtf(fmaf(sum, 1.f / D, eps)) : 1.f;
+    const F2 rr = f2(r, r);
+    F2 f[V / 2];
+    load_f2<V>(w + e0, f);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) u[i] = mul2(mul2(u[i], rr), f[i]);
+    load_f2<V>(w + e0 + gap, f);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = mul2(mul2(v[i], rr), f[i]);
+  }
+  rotation.turn(u, v);
+  row.u.set(u);
+  row.v.set(v);
+}
+
+template <typename T, bool CACHE>
+__device__ __forceinline__ int64_t rope_slot(const RopeArgs& a, int t) {
+  if (!CACHE) return -1;
+  const int slot = a.slots[t];
+  if (slot < 0 || slot >= a.cs.n_pages * a.cs.page_size) return -1;
+  const int page = slot / a.cs.page_size;
+  return page * a.cs.ps + (slot - page * a.cs.page_size) * a.cs.ts;
+}
+
+// Many tokens: warps walk tokens; queries, then keys, then (with a cache) values,
+// which are copied. The next step's row, of the next token too, is on its way
+// while a step is computed.
+template <typename T, int D, bool IL, bool CACHE, bool NORM, bool FULL>
+__global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_walk_kernel(const RopeArgs a) {
   constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
   dependency_release();
   dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const int l = lane % M::kLanes, grp = lane / M::kLanes;
-  const int heads = a.hq + a.hkv * (CACHE ? 2 : 1);
-  const int steps = (heads + M::kHeads - 1) / M::kHeads;
-  const int per = (steps + a.parts - 1) / a.parts;
-  const int items = a.n * a.parts, stride = gridDim.x * 4;
+  const int lane = threadIdx.x & 31, grp = lane / M::kLanes;
+  const int stride = gridDim.x * 4;
   int e0, e1;
-  rope_runs<V>(l, a.rot, &e0, &e1);
-  Raw<T, V> nu{}, nv{};
-  auto load = [&](int t, int h) {
-    const T* p;
-    if (h < a.hq)
-      p = static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs;
-    else if (h < a.hq + a.hkv)
-      p = static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
-    else if (CACHE && h < heads)
-      p = static_cast<const T*>(a.v) + t * a.vs.ts + (h - a.hq - a.hkv) * a.vs.hs;
-    else
-      return;
-    nu.load(p + e0);
-    nv.load(p + e1);
-  };
-  int item = blockIdx.x * 4 + (threadIdx.x >> 5);
-  int t = item / a.parts, st = (item % a.parts) * per;
-  if (item < items) load(t, st * M::kHeads + grp);
+  rope_runs<V>(lane % M::kLanes, a.rot, &e0, &e1);
+  const int gap = e1 - e0;
+  const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
+  const int k_steps = (a.hkv + M::kHeads - 1) / M::kHeads;
+  const T* const q0 = static_cast<const T*>(a.q) + grp * a.qs.hs + e0;
+  const T* const k0 = static_cast<const T*>(a.k) + grp * a.ks.hs + e0;
+  int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  RopeRow<T, V> next{};
+  if (t < a.n && grp < a.hq) next.load(q0 + t * a.qs.ts, gap);
+  const RopePairs<D, IL, V> pairs(a, lane);
+  int pos[M::kAngles] = {};
+  if (t < a.n) pairs.positions(a, t, pos);
   if constexpr (NORM) rope_weights<T, D>(a, weights);
-  RopeTurn<D, IL, V> rotation;
-  while (item < items) {
-    T *kc = nullptr, *vc = nullptr;
+  RopeTurn<D, IL, V, FULL> rotation;
+  for (; t < a.n; t += stride) {
+    const int t2 = t + stride;
+    const int64_t slot = rope_slot<T, CACHE>(a, t);
+    rotation.template set<false>(a, pairs, pos, lane);
+    if (t2 < a.n) pairs.positions(a, t2, pos);
+    const T* p = q0 + t * a.qs.ts;
+    T* o = static_cast<T*>(a.qo) + t * a.qos.ts + grp * a.qos.hs + e0;
+    for (int h = grp, st = 0; st < q_steps; ++st, h += M::kHeads) {
+      RopeRow<T, V> row = next;
+      p += M::kHeads * a.qs.hs;
+      if (st + 1 < q_steps) {
+        if (h + M::kHeads < a.hq) next.load(p, gap);
+      } else if (grp < a.hkv) {
+        next.load(k0 + t * a.ks.ts, gap);
+      }
+      rope_head<T, D, IL, NORM>(row, rotation, weights[0], a.wq != nullptr, e0, gap, a.eps);
+      if (h < a.hq) row.store(o, gap);
+      o += M::kHeads * a.qos.hs;
+    }
+    p = k0 + t * a.ks.ts;
+    const int64_t ostep = M::kHeads * (CACHE ? a.cs.hs : a.kos.hs);
+    o = CACHE ? static_cast<T*>(a.kc) + (slot + grp * a.cs.hs + e0)
+              : static_cast<T*>(a.ko) + t * a.kos.ts + grp * a.kos.hs + e0;
+    const T* const v0 = CACHE ? static_cast<const T*>(a.v) + t * a.vs.ts + grp * a.vs.hs + e0 : nullptr;
+    for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
+      RopeRow<T, V> row = next;
+      p += M::kHeads * a.ks.hs;
+      if (st + 1 < k_steps) {
+        if (h + M::kHeads < a.hkv) next.load(p, gap);
+      } else if (CACHE) {
+        if (grp < a.hkv) next.load(v0, gap);
+      } else if (t2 < a.n && grp < a.hq) {
+        next.load(q0 + t2 * a.qs.ts, gap);
+      }
+      rope_head<T, D, IL, NORM>(row, rotation, weights[NORM ? 1 : 0], a.wk != nullptr, e0, gap,
+                                   a.eps);
+      if (h < a.hkv && (!CACHE || slot >= 0)) row.store(o, gap);
+      o += ostep;
+    }
     if (CACHE) {
-      const int slot = a.slots[t];
-      if (slot >= 0 && slot < a.cs.n_pages * a.cs.page_size) {
-        const int64_t at = (int64_t)(slot / a.cs.page_size) * a.cs.ps +
-                           (int64_t)(slot % a.cs.page_size) * a.cs.ts;
-        kc = static_cast<T*>(a.kc) + at;
-        vc = static_cast<T*>(a.vc) + at;
+      p = v0;
+      o = static_cast<T*>(a.vc) + (slot + grp * a.cs.hs + e0);
+      for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
+        const RopeRow<T, V> row = next;
+        p += M::kHeads * a.vs.hs;
+        if (st + 1 < k_steps) {
+          if (h + M::kHeads < a.hkv) next.load(p, gap);
+        } else if (t2 < a.n && grp < a.hq) {
+          next.load(q0 + t2 * a.qs.ts, gap);
+        }
+        if (h < a.hkv && slot >= 0) row.store(o, gap);
+        o += ostep;
       }
     }
-    if (a.rot > 0) rotation.template set<false>(a, t, lane);
-    item += stride;
-    const int s1 = min(steps, st + per);
-    const int t2 = item / a.parts, st2 = (item % a.parts) * per;
-    for (; st < s1; ++st) {
-      const int h = st * M::kHeads + grp;
-      const bool is_q = h < a.hq, is_k = !is_q && h < a.hq + a.hkv;
-      Raw<T, V> cu = nu, cv = nv;
-      if (st + 1 < s1)
-        load(t, h + M::kHeads);
-      else if (item < items)
-        load(t2, st2 * M::kHeads + grp);
-      if (!CACHE || is_q || is_k || NORM) {
-        F2 u[V / 2], v[V / 2];
-        cu.get(u);
-        cv.get(v);
-        if constexpr (NORM) {
-          F2 ss = mul2(u[0], u[0]);
-#pragma unroll
-          for (int i = 1; i < V / 2; ++i) ss = fma2(u[i], u[i], ss);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) ss = fma2(v[i], v[i], ss);
-          const float2 two = unpack(ss);
-          const float sum = head_sum<M::kLanes>(two.x + two.y);
-          const float r = (is_q ? a.wq : a.wk) ? rsqrtf(sum * (1.f / D) + a.eps) : 1.f;
-          const F2 rr = f2(r, r);
-          F2 w[V / 2];
-          load_f2<V>(&weights[is_q ? 0 : 1][e0], w);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) u[i] = mul2(mul2(u[i], rr), w[i]);
-          load_f2<V>(&weights[is_q ? 0 : 1][e1], w);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) v[i] = mul2(mul2(v[i], rr), w[i]);
-        }
-        if (l < a.rot / (2 * V)) rotation.turn(u, v);
-        if (!CACHE || is_q || is_k) {
-          cu.set(u);
-          cv.set(v);
-        }
-      }
-      T* o = nullptr;
-      if (is_q)
-        o = static_cast<T*>(a.qo) + t * a.qos.ts + h * a.qos.hs;
-      else if (is_k)
-        o = CACHE ? (kc ? kc + (h - a.hq) * a.cs.hs : nullptr)
-                  : static_cast<T*>(a.ko) + t * a.kos.ts + (h - a.hq) * a.kos.hs;
-      else if (CACHE && h < heads && vc)
-        o = vc + (h - a.hq - a.hkv) * a.cs.hs;
-      if (o) {
-        cu.store(o + e0);
-        cv.store(o + e1);
-      }
-    }
-    t = t2;
-    st = st2;
   }
 }
 
-// Backward: warps walk tokens with a fixed stride, so the partial sums of the
-// weights' gradients have a fixed order; each block writes one row of them. Runs
-// of 4 elements (a lane holds half of what it would at 8, so more warps fit
-// beside the sums); the next step's rows are on their way while a step is
-// computed. dy in T2, x in T, dx in fp32.
-template <typename T, typename T2, int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(128, kBwdBlocksPerSm)
-    rope_bwd_kernel(const RopeArgs a, const void* dq, const void* dk, HeadRows dqs, HeadRows dks,
-                    float* gq, float* gk, float* part) {
-  constexpr int V = 4;
+// Few tokens, and keys and values alone (hq = 0): a warp per step of a token's heads.
+template <typename T, int D, bool IL, bool CACHE, bool NORM>
+__global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
+  constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
   dependency_release();
   dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int l = lane % M::kLanes, grp = lane / M::kLanes;
-  const int heads = a.hq + a.hkv;
-  const int steps = (heads + M::kHeads - 1) / M::kHeads;
+  const int lane = threadIdx.x & 31, grp = lane / M::kLanes;
+  const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
+  const int k_steps = (a.hkv + M::kHeads - 1) / M::kHeads;
+  const int steps = q_steps + k_steps * (CACHE ? 2 : 1);
+  const int item = blockIdx.x * 4 + (threadIdx.x >> 5), t = item / steps;
+  int st = item - t * steps, part = 0;  // 0 queries, 1 keys, 2 values
+  if (st >= q_steps) {
+    st -= q_steps;
+    part = 1;
+    if (CACHE && st >= k_steps) {
+      st -= k_steps;
+      part = 2;
+    }
+  }
+  const int h = st * M::kHeads + grp;
+  const bool mine = t < a.n && h < (part ? a.hkv : a.hq);
   int e0, e1;
-  rope_runs<V>(l, a.rot, &e0, &e1);
+  rope_runs<V>(lane % M::kLanes, a.rot, &e0, &e1);
+  const int gap = e1 - e0;
+  RopeRow<T, V> row{};
+  if (mine) {
+    const HeadRows s = part == 0 ? a.qs : part == 1 ? a.ks : a.vs;
+    row.load(static_cast<const T*>(part == 0 ? a.q : part == 1 ? a.k : a.v) + t * s.ts + h * s.hs +
+                 e0, gap);
+  }
+  if constexpr (NORM) rope_weights<T, D>(a, weights);
+  if (t >= a.n) return;
+  const int64_t slot = part ? rope_slot<T, CACHE>(a, t) : -1;
+  if (part < 2) {
+    const RopePairs<D, IL, V> pairs(a, lane);
+    int pos[M::kAngles];
+    pairs.positions(a, t, pos);
+    RopeTurn<D, IL, V> rotation;
+    rotation.template set<false>(a, pairs, pos, lane);
+    rope_head<T, D, IL, NORM>(row, rotation, weights[NORM ? part : 0],
+                                 (part ? a.wk : a.wq) != nullptr, e0, gap, a.eps);
+  }
+  if (!mine) return;
+  if (part == 0)
+    row.store(static_cast<T*>(a.qo) + t * a.qos.ts + h * a.qos.hs + e0, gap);
+  else if (!CACHE)
+    row.store(static_cast<T*>(a.ko) + t * a.kos.ts + h * a.kos.hs + e0, gap);
+  else if (slot >= 0)
+    row.store(static_cast<T*>(part == 1 ? a.kc : a.vc) + slot + h * a.cs.hs + e0, gap);
+}
+
+// Backward: warps walk tokens with a fixed stride, so the partial sums of the
+// weights' gradients have a fixed order; each block writes one row of them. The
+// next step's rows are on their way while a step is computed. dy in T2, x in T,
+// dx in fp32.
+template <typename T, typename T2, int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(128, kBwdBlocksPerSm)
+    rope_bwd_kernel(const RopeArgs a, const void* dq, const void* dk, HeadRows dqs, HeadRows dks,
+                    float* gq, float* gk, float* part) {
+  constexpr int V = kBwdRun;
+  using M = RopeMap<D, V>;
+  __shared__ __align__(16) float weights[2][NORM ? D : 1];
+  dependency_release();
+  dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / M::kLanes;
+  int e0, e1;
+  rope_runs<V>(lane % M::kLanes, a.rot, &e0, &e1);
+  const int gap = e1 - e0, stride = gridDim.x * 4;
+  const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
+  const int k_steps = (a.hkv + M::kHeads - 1) / M::kHeads;
+  const T2* const dq0 = static_cast<const T2*>(dq) + grp * dqs.hs + e0;
+  const T2* const dk0 = static_cast<const T2*>(dk) + grp * dks.hs + e0;
+  const T* const q0 = static_cast<const T*>(a.q) + grp * a.qs.hs + e0;
+  const T* const k0 = static_cast<const T*>(a.k) + grp * a.ks.hs + e0;
+  const bool has_q = NORM && a.wq, has_k = NORM && a.wk;
   F2 dwq[V] = {}, dwk[V] = {};
-  Raw<T2, V> nu{}, nv{};
-  Raw<T, V> nx{}, ny{};
-  auto load = [&](int t, int h) {
-    if (t >= a.n || h >= heads) return;
-    const bool is_q = h < a.hq;
-    const T2* p = is_q ? static_cast<const T2*>(dq) + t * dqs.ts + h * dqs.hs
-                       : static_cast<const T2*>(dk) + t * dks.ts + (h - a.hq) * dks.hs;
-    nu.load(p + e0);
-    nv.load(p + e1);
-    if (NORM && (is_q ? a.wq : a.wk)) {
-      const T* x = is_q ? static_cast<const T*>(a.q) + t * a.qs.ts + h * a.qs.hs
-                        : static_cast<const T*>(a.k) + t * a.ks.ts + (h - a.hq) * a.ks.hs;
-      nx.load(x + e0);
-      ny.load(x + e1);
+  RopeRow<T2, V> ndy{};
+  RopeRow<T, V> nx{};
+  auto first = [&](int t) {
+    if (t < a.n && grp < a.hq) {
+      ndy.load(dq0 + t * dqs.ts, gap);
+      if (has_q) nx.load(q0 + t * a.qs.ts, gap);
     }
   };
-  const int stride = gridDim.x * 4;
   int t = blockIdx.x * 4 + warp;
-  load(t, grp);
+  first(t);
+  const RopePairs<D, IL, V> pairs(a, lane);
+  int pos[M::kAngles] = {};
+  if (t < a.n) pairs.positions(a, t, pos);
   if constexpr (NORM) rope_weights<T, D>(a, weights);
   RopeTurn<D, IL, V> rotation;
+
+  // dx of a row from dy (in u, v) and x; its weights' gradient onto dw.
+  auto head = [&](const RopeRow<T2, V>& dy, const RopeRow<T, V>& xr, const float* w, bool has_w,
+                  F2 (&dw)[V], float* o, bool mine) {
+    F2 u[V / 2], v[V / 2];
+    dy.u.get(u);
+    dy.v.get(v);
+    rotation.turn(u, v);
+    if (NORM && has_w) {
+      F2 x[V / 2], y[V / 2], f[V / 2];
+      xr.u.get(x);
+      xr.v.get(y);
+      const float r = rsqrtf(fmaf(head_squares<V, M::kLanes>(x, y), 1.f / D, a.eps));
+      const F2 rr = f2(r, r);
+      F2 dd = f2(0.f, 0.f);
+      load_f2<V>(w + e0, f);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        x[i] = mul2(x[i], rr);
+        if (mine) dw[i] = fma2(u[i], x[i], dw[i]);
+        u[i] = mul2(u[i], f[i]);
+        dd = fma2(u[i], x[i], dd);
+      }
+      load_f2<V>(w + e1, f);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        y[i] = mul2(y[i], rr);
+        if (mine) dw[V / 2 + i] = fma2(v[i], y[i], dw[V / 2 + i]);
+        v[i] = mul2(v[i], f[i]);
+        dd = fma2(v[i], y[i], dd);
+      }
+      const float2 d2 = unpack(dd);
+      const float dot = head_sum<M::kLanes>(d2.x + d2.y) * (-1.f / D);
+      const F2 nd = f2(dot, dot);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        u[i] = mul2(rr, fma2(x[i], nd, u[i]));
+        v[i] = mul2(rr, fma2(y[i], nd, v[i]));
+      }
+    }
+    if (mine) {
+      RopeRow<float, V> out;
+      out.u.set(u);
+      out.v.set(v);
+      out.store(o, gap);
+    }
+  };
   for (; t < a.n; t += stride) {
-    if (a.rot > 0) rotation.template set<true>(a, t, lane);
-    for (int st = 0; st < steps; ++st) {
-      const int h = st * M::kHeads + grp;
-      const bool is_q = h < a.hq, is_k = !is_q && h < heads;
-      F2 u[V / 2], v[V / 2], x[V / 2], y[V / 2];
-      nu.get(u);
-      nv.get(v);
-      if (NORM) {
-        nx.get(x);
-        ny.get(y);
-      }
-      if (st + 1 < steps)
-        load(t, h + M::kHeads);
-      else
-        load(t + stride, grp);
-      if (l < a.rot / (2 * V)) rotation.turn(u, v);
-      if constexpr (NORM) {
-        const bool has_w = is_q ? a.wq != nullptr : is_k && a.wk != nullptr;
-        F2 ss = mul2(x[0], x[0]);
-#pragma unroll
-        for (int i = 1; i < V / 2; ++i) ss = fma2(x[i], x[i], ss);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) ss = fma2(y[i], y[i], ss);
-        const float2 s2 = unpack(ss);
-        const float r = rsqrtf(head_sum<M::kLanes>(s2.x + s2.y) * (1.f / D) + a.eps);
-        const F2 rr = f2(r, r);
-        F2 w[V / 2], dd = f2(0.f, 0.f);
-        if (has_w) {
-          load_f2<V>(&weights[is_q ? 0 : 1][e0], w);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            x[i] = mul2(x[i], rr);
-            if (is_q) dwq[i] = fma2(u[i], x[i], dwq[i]); else dwk[i] = fma2(u[i], x[i], dwk[i]);
-            u[i] = mul2(u[i], w[i]);
-            dd = fma2(u[i], x[i], dd);
-          }
-          load_f2<V>(&weights[is_q ? 0 : 1][e1], w);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            y[i] = mul2(y[i], rr);
-            if (is_q) dwq[V / 2 + i] = fma2(v[i], y[i], dwq[V / 2 + i]);
-            else dwk[V / 2 + i] = fma2(v[i], y[i], dwk[V / 2 + i]);
-            v[i] = mul2(v[i], w[i]);
-            dd = fma2(v[i], y[i], dd);
-          }
+    rotation.template set<true>(a, pairs, pos, lane);
+    if (t + stride < a.n) pairs.positions(a, t + stride, pos);
+    const T2* p = dq0 + t * dqs.ts;
+    const T* x = q0 + t * a.qs.ts;
+    float* o = gq + ((int64_t)t * a.hq + grp) * D + e0;
+    for (int h = grp, st = 0; st < q_steps; ++st, h += M::kHeads) {
+      const RopeRow<T2, V> dy = ndy;
+      const RopeRow<T, V> xr = nx;
+      p += M::kHeads * dqs.hs;
+      x += M::kHeads * a.qs.hs;
+      if (st + 1 < q_steps) {
+        if (h + M::kHeads < a.hq) {
+          ndy.load(p, gap);
+          if (has_q) nx.load(x, gap);
         }
-        const float2 d2 = unpack(dd);
-        const float dot = head_sum<M::kLanes>(d2.x + d2.y) * (-1.f / D);
-        const F2 nd = f2(dot, dot);
-        if (has_w) {
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            u[i] = mul2(rr, fma2(x[i], nd, u[i]));
-            v[i] = mul2(rr, fma2(y[i], nd, v[i]));
-          }
+      } else if (grp < a.hkv) {
+        ndy.load(dk0 + t * dks.ts, gap);
+        if (has_k) nx.load(k0 + t * a.ks.ts, gap);
+      }
+      head(dy, xr, weights[0], has_q, dwq, o, h < a.hq);
+      o += M::kHeads * D;
+    }
+    p = dk0 + t * dks.ts;
+    x = k0 + t * a.ks.ts;
+    o = gk + ((int64_t)t * a.hkv + grp) * D + e0;
+    for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
+      const RopeRow<T2, V> dy = ndy;
+      const RopeRow<T, V> xr = nx;
+      p += M::kHeads * dks.hs;
+      x += M::kHeads * a.ks.hs;
+      if (st + 1 < k_steps) {
+        if (h + M::kHeads < a.hkv) {
+          ndy.load(p, gap);
+          if (has_k) nx.load(x, gap);
         }
+      } else {
+        first(t + stride);
       }
-      if (is_q || is_k) {
-        float* o = is_q ? gq + ((int64_t)t * a.hq + h) * D
-                        : gk + ((int64_t)t * a.hkv + (h - a.hq)) * D;
-        Raw<float, V> raw;
-        raw.set(u);
-        raw.store(o + e0);
-        raw.set(v);
-        raw.store(o + e1);
-      }
+      head(dy, xr, weights[NORM ? 1 : 0], has_k, dwk, o, h < a.hkv);
+      o += M::kHeads * D;
     }
   }
   if constexpr (NORM) {
@@ -471,27 +610,30 @@ void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions
 }
 
 template <typename T, int D, bool CACHE, bool NORM>
-cudaError_t launch_rope(RopeArgs a, bool il, int sms, cudaStream_t s) {
-  const int heads = a.hq + a.hkv * (CACHE ? 2 : 1);
-  const int steps = (heads + RopeMap<D, kRopeRun>::kHeads - 1) / RopeMap<D, kRopeRun>::kHeads;
-  // Items per token: one, two, or one per step of heads, whichever gives the longest walk
-  // of a warp the least to do; an item's angles count as a step and a half.
+cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
+  constexpr int H = RopeMap<D, kRopeRun>::kHeads;
+  const int64_t q_steps = (a.hq + H - 1) / H, k_steps = (a.hkv + H - 1) / H;
+  const int64_t steps = q_steps + k_steps * (CACHE ? 2 : 1), n = a.n;
+  // A warp per step while that gives the longest-running warp less to do than walking whole
+  // tokens; a token's angles count as a step and a half.
   const int64_t warps = (int64_t)sms * kRopeBlocks<T> * 4;
-  double best = 0.;
-  for (int parts : {1, 2, steps}) {
-    if (parts > steps || (int64_t)a.n * parts > INT32_MAX / 2) continue;
-    const int per = (steps + parts - 1) / parts;
-    const double cost = (double)(((int64_t)a.n * parts + warps - 1) / warps) * (per + 1.5);
-    if (a.parts == 0 || cost < best) {
-      best = cost;
-      a.parts = parts;
-    }
-  }
-  const int64_t want = ((int64_t)a.n * a.parts + 3) / 4, most = (int64_t)sms * kRopeBlocks<T>;
-  const dim3 grid((unsigned)(want < most ? want : most)), block(128);
+  const bool walk = a.hq > 0 && ((n + warps - 1) / warps) * (steps + 1.5) <
+                                    ((n * steps + warps - 1) / warps) * 2.5;
   const char* name = CACHE ? "qk_rope_append" : "qk_rope";
-  if (il) return launch_after(name, rope_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a);
-  return launch_after(name, rope_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
+  const dim3 block(128);
+  if (walk) {
+    const int64_t want = (n + 3) / 4, most = (int64_t)sms * kRopeBlocks<T>;
+    const dim3 grid((unsigned)(want < most ? want : most));
+    auto* kernel = a.rot == D ? (il ? rope_walk_kernel<T, D, true, CACHE, NORM, true>
+                                    : rope_walk_kernel<T, D, false, CACHE, NORM, true>)
+                              : (il ? rope_walk_kernel<T, D, true, CACHE, NORM, false>
+                                    : rope_walk_kernel<T, D, false, CACHE, NORM, false>);
+    return launch_after(name, kernel, grid, block, 0, s, a);
+  }
+  if (n * steps > INT32_MAX - 3) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((n * steps + 3) / 4));
+  return il ? launch_after(name, rope_step_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a)
+            : launch_after(name, rope_step_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
 }
 
 template <typename T, int D, bool CACHE>

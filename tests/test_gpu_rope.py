@@ -82,6 +82,8 @@ CASES = [
     (50, 16, 1, 128, BF16, 0, False, "qk", 1, "fused"),
     (2500, 7, 7, 64, FP32, 64, True, "qk", 1, "dense"),
     (5001, 12, 2, 128, BF16, 96, False, "qk", 3, "fused"),
+    (4300, 5, 5, 128, BF16, 128, True, "k", 1, "heads"),
+    (3700, 3, 1, 64, FP32, 64, False, None, 3, "fused"),
 ]
 
 
@@ -165,11 +167,33 @@ def test_a_bad_row_stays_alone():
     assert torch.equal(k[keep], k0[keep])
 
 
+@pytest.mark.parametrize("n", [3, 9000])
+@pytest.mark.parametrize("il", [False, True])
+def test_a_bad_element_reaches_its_pair_alone(n, il):
+    """Without a norm a NaN or an infinity spoils its pair; the rest of the head,
+    the part beyond the rotation too, is as without it. 9000 tokens: the walk
+    over tokens, 3: a warp per step."""
+    c = (n, 4, 2, 64, FP32, 32, il, None, 1, "dense")
+    Q, K, _, _, _, args, kw, _ = _case(c)
+    q0, k0 = fb.qk_rope(Q, K, *args, **kw)
+    bad = [(0, 1, 40, float("inf")), (n - 1, 3, 63, float("nan")), (1, 0, 5, float("inf"))]
+    for t, h, e, x in bad:
+        Q[t, h, e] = x
+        K[t, h % 2, e] = x
+    q, k = fb.qk_rope(Q, K, *args, **kw)
+    for got, want, heads in ((q, q0, 4), (k, k0, 2)):
+        keep = torch.ones_like(got, dtype=torch.bool)
+        for t, h, e, _ in bad:
+            pair = ([e] if e >= 32 else [e & ~1, e | 1] if il else [e % 16, e % 16 + 16])
+            keep[t, h % heads, pair] = False
+        assert torch.equal(got[keep], want[keep]) and not torch.isfinite(got[~keep]).any()
+
+
 # --------------------------------------------------------------------- into the cache
 @pytest.mark.parametrize("heads_outer", [False, True])
 @pytest.mark.parametrize("page", [1, 16, 23])
-@pytest.mark.parametrize("c", [CASES[0], CASES[1], CASES[3], CASES[5], CASES[9], CASES[10]],
-                         ids=str)
+@pytest.mark.parametrize("c", [CASES[0], CASES[1], CASES[3], CASES[5], CASES[9], CASES[10],
+                               CASES[11], CASES[12], CASES[13]], ids=str)
 def test_append(c, page, heads_outer):
     """The outputs of qk_rope, bit for bit, at their slots; every other element
     of the cache as it was; slots outside the cache written nowhere."""
