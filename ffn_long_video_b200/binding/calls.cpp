@@ -16,6 +16,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <cmath>
 #include <exception>
 #include <initializer_list>
@@ -254,6 +255,51 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device device) 
   return at::empty(shape, at::TensorOptions().dtype(type).device(device));
 }
 
+// Several dense tensors to be written. Small ones share one allocation, each on a
+// 256-byte boundary (an allocation costs a call 0.8 us); large ones have their
+// own, so that keeping one of them does not keep the others' memory.
+struct Piece {
+  at::SmallVector<int64_t, 3> shape;
+  at::ScalarType type;
+};
+template <size_t N>
+std::array<at::Tensor, N> make_all(const std::array<Piece, N>& pieces, c10::Device device) {
+  constexpr int64_t kShared = 1 << 20;
+  int64_t first[N], bytes = 0;
+  for (size_t i = 0; i < N; ++i) {
+    int64_t n = (int64_t)c10::elementSize(pieces[i].type);
+    for (int64_t d : pieces[i].shape) n *= d;
+    first[i] = bytes;
+    bytes += (n + 255) / 256 * 256;
+  }
+  std::array<at::Tensor, N> r;
+  if (bytes > kShared) {
+    for (size_t i = 0; i < N; ++i) r[i] = make(pieces[i].shape, pieces[i].type, device);
+    return r;
+  }
+  const at::Tensor all = make({bytes}, at::kByte, device);
+  for (size_t i = 0; i < N; ++i) {
+    r[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                    c10::scalarTypeToTypeMeta(pieces[i].type));
+    r[i].unsafeGetTensorImpl()->set_sizes_contiguous(pieces[i].shape);
+    r[i].unsafeGetTensorImpl()->set_storage_offset(
+        first[i] / (int64_t)c10::elementSize(pieces[i].type));
+  }
+  return r;
+}
+// Two of them, where neither is given.
+void make_two(at::Tensor& x, const at::Tensor* given_x, const Piece& px, at::Tensor& y,
+              const at::Tensor* given_y, const Piece& py, c10::Device device) {
+  if (!given_x && !given_y) {
+    auto r = make_all<2>({{px, py}}, device);
+    x = std::move(r[0]);
+    y = std::move(r[1]);
+  } else {
+    x = given_x ? *given_x : make(px.shape, px.type, device);
+    y = given_y ? *given_y : make(py.shape, py.type, device);
+  }
+}
+
 void done(int rc, const char* what) {
   if (rc == ADASPARK_OK) return;
   PyObject* e = g_error ? PyObject_CallFunction(g_error, "is", rc, what) : nullptr;
@@ -324,8 +370,8 @@ PyObject* py_qk_rope(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     const int64_t qs[3] = {q.n, q.h, q.d}, ks[3] = {q.n, k.h, q.d};
     const Rows rq(Q, "Q", of.type, of.device, qs), rk(K, "K", of.type, of.device, ks);
     const Rope r(pos, freq, wq, wk, eps, il, sections, mag, of.type, of.device, q.n, q.d);
-    const at::Tensor Qo = oq ? *oq : make(qs, of.type, of.device);
-    const at::Tensor Ko = ok ? *ok : make(ks, of.type, of.device);
+    at::Tensor Qo, Ko;
+    make_two(Qo, oq, {{q.n, q.h, q.d}, of.type}, Ko, ok, {{q.n, k.h, q.d}, of.type}, of.device);
     const Rows wo(Qo, "out_q", of.type, of.device, qs), wko(Ko, "out_k", of.type, of.device, ks);
     done(adaspark_qk_rope(rq.p, rq.ts, rq.hs, rk.p, rk.ts, rk.hs, of.code, r.pos, r.axes, r.sec,
                           r.freq, r.rot, r.interleaved, r.magnitude, r.wq, r.wk, r.eps, q.n, q.h,
@@ -422,11 +468,15 @@ PyObject* py_qk_rope_backward(PyObject*, PyObject* const* argv, Py_ssize_t argc)
     const Rows rq = wq ? Rows(*Q, "Q", of.type, dy.device, qs) : Rows();
     const Rows rk = wk ? Rows(*K, "K", of.type, dy.device, ks) : Rows();
     const Rope r(pos, freq, wq, wk, eps, il, sections, mag, of.type, dy.device, q.n, q.d);
-    const at::Tensor dQ = tq ? *tq : make(qs, at::kFloat, dy.device);
-    const at::Tensor dK = tk ? *tk : make(ks, at::kFloat, dy.device);
-    at::Tensor dwq, dwk, ws;
-    if (wq) dwq = twq ? *twq : make({q.d}, at::kFloat, dy.device);
-    if (wk) dwk = twk ? *twk : make({q.d}, at::kFloat, dy.device);
+    at::Tensor dQ, dK, dwq, dwk, ws;
+    make_two(dQ, tq, {{q.n, q.h, q.d}, at::kFloat}, dK, tk, {{q.n, k.h, q.d}, at::kFloat},
+             dy.device);
+    if (wq && wk) {
+      make_two(dwq, twq, {{q.d}, at::kFloat}, dwk, twk, {{q.d}, at::kFloat}, dy.device);
+    } else {
+      if (wq) dwq = twq ? *twq : make({q.d}, at::kFloat, dy.device);
+      if (wk) dwk = twk ? *twk : make({q.d}, at::kFloat, dy.device);
+    }
     if (tws) {
       ws = *tws;
     } else if (w) {
@@ -481,10 +531,20 @@ PyObject* py_kv_plan(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     int32_t* pnf = ints(n_free, "n_free", 1);
     const size_t nb = adaspark_kv_plan_workspace((int)ns);
     if (nb == 0 || rows < 1) done(ADASPARK_EINVAL, "adaspark_kv_plan");
-    const at::Tensor slots = ts ? *ts : make({rows}, at::kInt, dev);
-    const at::Tensor positions = tp ? *tp : make({rows}, at::kInt, dev);
-    const at::Tensor starts = tt ? *tt : make({ns + 1}, at::kInt, dev);
-    const at::Tensor ws = tw ? *tw : make({(int64_t)nb}, at::kByte, dev);
+    at::Tensor slots, positions, starts, ws;
+    if (!ts && !tp && !tt && !tw) {
+      auto r = make_all<4>({{{{rows}, at::kInt}, {{rows}, at::kInt}, {{ns + 1}, at::kInt},
+                             {{(int64_t)nb}, at::kByte}}}, dev);
+      slots = std::move(r[0]);
+      positions = std::move(r[1]);
+      starts = std::move(r[2]);
+      ws = std::move(r[3]);
+    } else {
+      slots = ts ? *ts : make({rows}, at::kInt, dev);
+      positions = tp ? *tp : make({rows}, at::kInt, dev);
+      starts = tt ? *tt : make({ns + 1}, at::kInt, dev);
+      ws = tw ? *tw : make({(int64_t)nb}, at::kByte, dev);
+    }
     const Workspace w(ws, dev);
     done(adaspark_kv_plan(po, pn, (int)ns, page, tb.p, tb.stride, tb.cols, pf, (int)pages, pnf,
                           ints(starts, "token_starts", ns + 1), ints(slots, "slots", rows),
@@ -524,8 +584,8 @@ PyObject* py_decode_attn(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     }
     const size_t nb = adaspark_decode_attn_workspace(q.n, q.h, hkv, q.d, of.code);
     if (nb == 0) done(ADASPARK_EINVAL, "adaspark_decode_attn_workspace");
-    const at::Tensor out = to ? *to : make(qs, of.type, of.device);
-    const at::Tensor lse = tl ? *tl : make({q.n, q.h}, at::kFloat, of.device);
+    at::Tensor out, lse;
+    make_two(out, to, {{q.n, q.h, q.d}, of.type}, lse, tl, {{q.n, q.h}, at::kFloat}, of.device);
     const at::Tensor ws = tw ? *tw : make({(int64_t)nb}, at::kByte, of.device);
     const Workspace w(ws, of.device);
     done(adaspark_decode_attn(rq.p, rq.ts, rq.hs, c.k, c.v, c.ps, c.ts, c.hs, c.pages, c.page,

@@ -938,13 +938,14 @@ DecLayout dec_layout(int d) {
   return L;
 }
 
+int64_t dec_run_tiles(int64_t max_len, int tile) { return (max_len + tile - 1) / tile; }
+
 template <class M>
 int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   using S = typename M::S;
   // no more blocks than tiles the tables can hold
   const int64_t runs = (int64_t)a.n_seqs * a.hkv * a.hgroups;
-  const int64_t tiles = runs * (((int64_t)a.max_len + S::kTile - 1) / S::kTile);
-  if (tiles > INT32_MAX) return ADASPARK_EINVAL;
+  const int64_t tiles = runs * dec_run_tiles(a.max_len, S::kTile);
   int64_t grid = S::kBlocks * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;
   if (grid > tiles) grid = tiles;
@@ -975,7 +976,7 @@ using namespace adaspark;
 extern "C" {
 
 size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dtype) {
-  if (n_seqs < 1 || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
   return dec_layout(d).total;
 }
 
@@ -986,11 +987,16 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
                          int hq, int hkv, int d, float scale, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, void* stream) {
   if (!Q || !block_table || !seq_lens || !out || !workspace) return ADASPARK_EINVAL;
-  if (n_seqs < 1 || max_pages < 1 || !head_sizes_ok(hq, hkv, d, dtype)) return ADASPARK_EINVAL;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs || max_pages < 1 || !head_sizes_ok(hq, hkv, d, dtype)) return ADASPARK_EINVAL;
   if (!std::isfinite(scale)) return ADASPARK_EINVAL;
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
   if (!cache_ok(k_cache, v_cache, cs, hkv, d, dtype)) return ADASPARK_EINVAL;
   if ((int64_t)max_pages * page_size > INT32_MAX - 1024) return ADASPARK_EINVAL;
+  const int hgroups = (hq / hkv + kDecHeads - 1) / kDecHeads;
+  const int tile = 4096 / (d * (int)elem_size(dtype)) * kDecWarps;
+  if ((int64_t)n_seqs * hkv * hgroups * dec_run_tiles((int64_t)max_pages * page_size, tile) >
+      INT32_MAX)
+    return ADASPARK_EINVAL;
   if (!rows_aligned(Q, q_ts, q_hs, dtype) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return ADASPARK_EINVAL;
@@ -1011,7 +1017,7 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
   a.n_seqs = n_seqs; a.max_len = max_pages * page_size;
   a.hq = hq; a.hkv = hkv; a.group = hq / hkv;
-  a.hgroups = (a.group + kDecHeads - 1) / kDecHeads;
+  a.hgroups = hgroups;
   a.status = reinterpret_cast<int32_t*>(ws + L.status);
   a.joins = reinterpret_cast<int4*>(ws + L.joins);
   a.part = reinterpret_cast<float*>(ws + L.part);

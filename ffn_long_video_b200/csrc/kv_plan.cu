@@ -311,7 +311,7 @@ using namespace adaspark;
 extern "C" {
 
 size_t adaspark_kv_plan_workspace(int n_seqs) {
-  if (n_seqs < 1) return 0;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
   return align_up(sizeof(WsHeader)) + 2 * align_up((size_t)n_seqs * sizeof(int32_t));
 }
 
@@ -327,6 +327,8 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
     return ADASPARK_EINVAL;
   if (table_stride < max_pages && n_seqs > 1) return ADASPARK_EINVAL;
   if ((int64_t)n_pages * page_size > INT32_MAX) return ADASPARK_EINVAL;
+  // room for the kernels' strides in 32 bits
+  if (n_seqs > kMaxSeqs || n_pages > (1 << 30) || n_rows > (1 << 30)) return ADASPARK_EINVAL;
   for (const void* p : {(const void*)old_lens, (const void*)new_lens, (const void*)block_table,
                         (const void*)free_pages, (const void*)n_free, (const void*)token_starts,
                         (const void*)slots, (const void*)positions})

@@ -554,24 +554,28 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   }
 }
 
-// Sums the blocks' rows, 32 columns per block: column c of rows y, y + 32, ...
+// Sums the blocks' rows, 8 columns per block: column c of rows y, y + 128, ..., then
+// over y in halves.
 __global__ void __launch_bounds__(1024)
     rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
-  __shared__ float sum[32][33];
+  __shared__ float sum[128][9];
   dependency_release();
   dependency_wait();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + x;
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int col = blockIdx.x * 8 + x;
   float acc = 0.f;
-  for (int r = y; r < rows; r += 32) acc += part[(int64_t)r * 2 * d + col];
+#pragma unroll 6
+  for (int r = y; r < rows; r += 128) acc += part[(int64_t)r * 2 * d + col];
   sum[y][x] = acc;
   __syncthreads();
-  if (y == 0) {
-    acc = 0.f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) acc += sum[r][x];
+  for (int half = 64; half > 0; half >>= 1) {
+    if (y < half) sum[y][x] += sum[y + half][x];
+    __syncthreads();
+  }
+  if (y == 0) {
     float* o = col < d ? dwq : dwk;
-    if (o) o[col % d] = acc;
+    if (o) o[col % d] = sum[0][x];
   }
 }
 
@@ -869,7 +873,7 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     e = dy_dtype == ADASPARK_BF16 ? dispatch_bwd<float, bf16>(b, d, il, s)
                                   : dispatch_bwd<float, float>(b, d, il, s);
   if (e == cudaSuccess && norm)
-    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 32), dim3(1024), 0, s, b.part, blocks, d,
+    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 8), dim3(1024), 0, s, b.part, blocks, d,
                w_q ? dw_q : nullptr, w_k ? dw_k : nullptr);
   return cuda_status(e);
 }

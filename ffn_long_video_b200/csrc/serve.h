@@ -18,6 +18,8 @@ struct CacheRows {
   int32_t n_pages, page_size;
 };
 
+constexpr int kMaxSeqs = 1 << 24;  // sequences of a plan or a decode call
+
 inline size_t elem_size(int dtype) { return dtype == ADASPARK_BF16 ? 2 : 4; }
 
 // The kernels move 16 bytes at a time: a 16-byte base and strides of whole 16 bytes.

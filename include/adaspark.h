@@ -621,7 +621,8 @@ size_t adaspark_kv_plan_workspace(int n_seqs);
  * a free count or a gift the pool cannot hold); a page number outside
  * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. The arrays
  * must not overlap. workspace: 256-byte aligned. ADASPARK_EINVAL for NULL
- * pointers, sizes < 1, a table_stride below max_pages, a short workspace. */
+ * pointers, sizes < 1, n_seqs > 2^24, n_pages or n_rows > 2^30, a table_stride
+ * below max_pages, a short workspace. */
 int adaspark_kv_plan(const int32_t *old_lens, const int32_t *new_lens, int n_seqs, int page_size,
                      int32_t *block_table, int64_t table_stride, int max_pages,
                      int32_t *free_pages, int n_pages, int32_t *n_free, int32_t *token_starts,
@@ -648,7 +649,7 @@ size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dt
  * Results depend on the inputs, the sizes and max_pages alone (no atomics). A
  * length out of range counts as 0 and a page number outside [0, n_pages) as
  * absent keys; both report ADASPARK_DEV_BAD_LAYOUT. Errors: ADASPARK_EINVAL as
- * for the other calls, n_seqs or max_pages < 1, or tables that could hold 2^31
+ * for the other calls, n_seqs or max_pages < 1, n_seqs > 2^24, or tables that could hold 2^31
  * tiles of 32 keys and 8 query heads, over all sequences and KV heads. */
 int adaspark_decode_attn(const void *Q, int64_t q_ts, int64_t q_hs, const void *k_cache,
                          const void *v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,

@@ -159,7 +159,7 @@ ROPE_BAD = [dict(Q=None), dict(K=None), dict(pos=None), dict(freq=None), dict(n=
             dict(rot=-16), dict(axes=2), dict(axes=3, sec=BAD_SEC), dict(axes=3, sec=NEG_SEC),
             dict(axes=3, sec=None), dict(eps=-1.0), dict(eps=float("nan")),
             dict(mag=float("inf")), dict(Q=ODD), dict(q_ts=1028), dict(k_hs=132), dict(wq=ODD),
-            dict(hq=8192, hkv=2)]
+            dict(hq=8192, hkv=2), dict(n=(1 << 30) + 1)]
 ROPE_OUT_BAD = [dict(Qo=None), dict(Qo=ODD), dict(qo_ts=1028),
                 dict(qo_ts=512), dict(qo_hs=64), dict(qo_ts=0)]   # rows that share memory
 CACHE = dict(slots=P, kc=P, vc=P, c_ps=4096, c_ts=256, c_hs=128, pages=50, page=16)
@@ -222,7 +222,9 @@ PLAN_ORDER = "old new ns page table ts cols free pages nf starts slots pos rows 
 @pytest.mark.parametrize("change", [{k: None} for k in "old new table free nf starts slots pos ws".split()]
                          + [{k: 0} for k in "ns page cols pages rows wsb".split()]
                          + [dict(ts=7), dict(old=ctypes.c_void_p(4097)),
-                            dict(ws=ctypes.c_void_p(4097)), dict(pages=1 << 20, page=1 << 12)])
+                            dict(ws=ctypes.c_void_p(4097)), dict(pages=1 << 20, page=1 << 12),
+                            dict(ns=(1 << 24) + 1, wsb=1 << 40), dict(rows=(1 << 30) + 1),
+                            dict(pages=(1 << 30) + 1, page=1)])
 def test_kv_plan_refusals(change):
     base = dict(old=P, new=P, ns=5, page=16, table=P, ts=8, cols=8, free=P, pages=64, nf=P,
                 starts=P, slots=P, pos=P, rows=40, ws=P, wsb=fb.kv_plan_workspace_bytes(5),
@@ -238,7 +240,9 @@ DECODE_ORDER = ("Q q_ts q_hs kc vc c_ps c_ts c_hs pages page dtype table ts cols
                                     dict(ws=None), dict(wsb=100), dict(ns=0), dict(cols=0),
                                     dict(scale=float("nan")), dict(hq=9), dict(d=256), dict(Q=ODD),
                                     dict(q_ts=1028), dict(out=ODD), dict(dtype=3),
-                                    dict(cols=1 << 28), dict(ws=ctypes.c_void_p(4097))]
+                                    dict(cols=1 << 28), dict(ws=ctypes.c_void_p(4097)),
+                                    dict(ns=(1 << 24) + 1, wsb=1 << 40),
+                                    dict(ns=1 << 23, cols=1 << 16, wsb=1 << 40)]
                          + CACHE_BAD[1:])
 def test_decode_attn_refusals(change):
     base = dict(Q=P, q_ts=1024, q_hs=128, dtype=fb.BF16, table=P, ts=8, cols=8, lens=P, ns=5, hq=8,
