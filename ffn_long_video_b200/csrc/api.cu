@@ -567,9 +567,21 @@ int adaspark_read_device_status(const void* workspace, uint32_t* detail, void* s
   if (!workspace) return ADASPARK_EINVAL;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return ADASPARK_ECUDA;
-  uint32_t st[2] = {0, 0};
-  if (cudaMemcpy(st, workspace, sizeof(st), cudaMemcpyDeviceToHost) != cudaSuccess)
+  WsHeader h;
+  if (cudaMemcpy(&h, workspace, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess)
     return ADASPARK_ECUDA;
+  uint32_t st[2] = {h.status, h.detail};
+  constexpr uint32_t kMost = 1024;
+  if (h.n_block_status > 0 && h.n_block_status <= kMost) {
+    uint32_t words[kMost];
+    if (cudaMemcpy(words, static_cast<const uint8_t*>(workspace) + sizeof(h),
+                   h.n_block_status * sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+      return ADASPARK_ECUDA;
+    for (uint32_t i = 0; i < h.n_block_status; ++i) {
+      if (words[i] && !st[0]) st[1] = 0x9100u + i;
+      st[0] |= words[i];
+    }
+  }
   if (detail) *detail = (st[0] & 0xffu) | ((st[1] & 0xffffu) << 8);
   return st[0] ? ADASPARK_EDEVICE : ADASPARK_OK;
 }

@@ -21,7 +21,9 @@ struct WsHeader {
   uint32_t m_active;      // FFN: number of active rows (visual + text)
   uint32_t sched[4];      // persistent-kernel tile counters
   uint64_t stats[16];     // adaspark_attn_stats / adaspark_ffn_stats
-  uint32_t pad[24];
+  uint32_t pad[23];
+  uint32_t n_block_status; // status words of single blocks, behind the header; they count
+                           // like `status` (0 where a call has none)
 };
 static_assert(sizeof(WsHeader) == 256, "header must be 256 bytes");
 

@@ -51,6 +51,7 @@ struct DecodeArgs {
 constexpr int kDecHeads = 8;     // query heads of a run
 constexpr int kDecWarps = 4;
 constexpr int kDecMaxBlocks = 148 * 3;
+constexpr int kDecCluster = 8;   // blocks that join through shared memory, at most
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
@@ -180,6 +181,22 @@ __device__ __forceinline__ DecLine dec_begin(const DecodeArgs& a, DecShared& sh,
   }
   __syncthreads();
   return L;
+}
+
+// The block's status word; block 0 writes the header that counts them. All threads.
+__device__ __forceinline__ void dec_status(const DecodeArgs& a, DecShared& sh, uint32_t bits) {
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if ((threadIdx.x & 31) == 0) sh.bits[threadIdx.x >> 5] = bits;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t v = 0;
+    for (int w = 0; w < kDecWarps; ++w) v |= sh.bits[w];
+    a.status[blockIdx.x] = (int32_t)v;
+    if (blockIdx.x == 0) {
+      a.hdr->status = a.hdr->detail = 0;
+      a.hdr->n_block_status = gridDim.x;
+    }
+  }
 }
 
 // Next run on the line (seq = n_seqs behind the last one).
@@ -427,15 +444,149 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks) decode_kernel(c
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
     }
   }
-  bits = __reduce_or_sync(0xffffffffu, bits);
-  if ((threadIdx.x & 31) == 0) sh.bits[warp] = bits;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t v = 0;
-    for (int w = 0; w < kDecWarps; ++w) v |= sh.bits[w];
-    a.status[blockIdx.x] = (int32_t)v;
-    if (!a.by_run) a.joins[blockIdx.x] = join;
+  dec_status(a, sh, bits);
+  if (threadIdx.x == 0 && !a.by_run) a.joins[blockIdx.x] = join;
+}
+
+// Address of a peer block's shared memory, loads from it, and the cluster's barrier.
+__device__ __forceinline__ uint32_t peer_smem(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_load(uint32_t address) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(address) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// Few short runs: a cluster of blocks per run (no line to lay out), each with an
+// even share of its tiles; the parts are joined through the blocks' shared memory
+// and there is no second kernel. All branches around the barriers go by the
+// sequence's length, which the cluster shares.
+template <class M>
+__global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
+    decode_cluster_kernel(const DecodeArgs a, int C) {
+  using S = typename M::S;
+  using T = typename S::T;
+  constexpr int D = S::D, E = D / 32;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ DecShared sh;
+  __shared__ typename M::Shared msh;
+  __shared__ float part[kDecHeads][D + 2];   // this block's outputs, maxima, sums
+  dependency_release();
+  dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = blockIdx.x % C, runs = a.hkv * a.hgroups;
+  uint32_t bits = 0;
+  DecSpot at;
+  at.seq = blockIdx.x / C / runs;
+  at.run = blockIdx.x / C - at.seq * runs;
+  at.len = dec_len(a, at.seq, &bits);
+  at.tiles = (at.len + S::kTile - 1) / S::kTile;
+  const int heads = min(kDecHeads, a.group - at.run % a.hgroups * kDecHeads);
+  const int64_t row0 = (int64_t)at.seq * a.hq + at.run / a.hgroups * a.group +
+                       at.run % a.hgroups * kDecHeads;
+  if (at.len == 0) {
+    if (rank == 0) {
+      for (int e = threadIdx.x; e < heads * D; e += kDecWarps * 32)
+        static_cast<T*>(a.out)[row0 * D + e] = from_f32<T>(0.f);
+      if (a.lse && threadIdx.x < heads) a.lse[row0 + threadIdx.x] = -INFINITY;
+    }
+  } else {
+    at.tile = at.tiles * rank / C;
+    const int steps = at.tiles * (rank + 1) / C - at.tile;
+    uint8_t* ring = smem + warp * S::kRing;
+    DecWalk<S> ahead(a, at);
+    uint32_t there[S::kStages - 1];
+    DecRow row[S::kStages];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) {
+      if (i < steps) row[i] = ahead.row();
+      if (i + 1 < steps) ahead.next(a, &bits);
+    }
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i)
+      there[i] = dec_copy<S>(a, ring + i * S::kStage, row[i], i < steps, &bits);
+    DecRow next = row[S::kStages - 1];
+    M math(a, msh);
+    math.begin(at);
+    int stage = 0;
+    for (int i = 0; i < steps; ++i) {
+      __syncwarp();
+      const uint32_t coming =
+          dec_copy<S>(a, ring + (stage == 0 ? S::kStages - 1 : stage - 1) * S::kStage, next,
+                      i + S::kStages - 1 < steps, &bits);
+      if (i + S::kStages < steps) {
+        next = ahead.row();
+        if (i + S::kStages + 1 < steps) ahead.next(a, &bits);
+      }
+      cp_async_wait<S::kStages - 1>();
+      __syncwarp();
+      math.tile(ring + stage * S::kStage, there[0]);
+#pragma unroll
+      for (int k = 0; k < S::kStages - 2; ++k) there[k] = there[k + 1];
+      there[S::kStages - 2] = coming;
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    }
+    // the warps' parts into the block's; nothing is in flight any more
+    math.sums(sh.m[warp], sh.l[warp]);
+    __syncwarp();
+    math.outputs(reinterpret_cast<float*>(ring));
+    __syncthreads();
+    for (int h = warp; h < heads; h += kDecWarps) {
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) mm = fmaxf(mm, sh.m[w][h]);
+      const float mu = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f, acc[E] = {};
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float f = exp2f(sh.m[w][h] - mu);
+        ll = fmaf(sh.l[w][h], f, ll);
+        const float* o = reinterpret_cast<const float*>(smem + w * S::kRing);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[h * (D + 4) + 32 * e + lane], f, acc[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[h][32 * e + lane] = acc[e];
+      if (lane == 0) {
+        part[h][D] = mm;
+        part[h][D + 1] = ll;
+      }
+    }
+    cluster_barrier();
+    // the blocks' parts, in order: head h by block h % C, warp h / C
+    for (int h = rank + C * warp; h < heads; h += C * kDecWarps) {
+      const uint32_t peer = peer_smem(part[h], min(lane, C - 1));
+      float m = peer_load(peer + D * 4), l = peer_load(peer + D * 4 + 4);
+      if (lane >= C) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      const float mm = warp_max(m), mu = mm == -INFINITY ? 0.f : mm;
+      const float f = lane < C ? exp2f(m - mu) : 0.f, ll = warp_sum(l * f);
+      float acc[E] = {};
+      for (int p = 0; p < C; ++p) {
+        const uint32_t from = peer_smem(part[h], p);
+        const float w = __shfl_sync(0xffffffffu, f, p);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(peer_load(from + (32 * e + lane) * 4), w, acc[e]);
+      }
+      const float r = 1.f / ll;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        static_cast<T*>(a.out)[(row0 + h) * D + 32 * e + lane] =
+            from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
+      if (a.lse && lane == 0) a.lse[row0 + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    }
+    cluster_barrier();  // no block leaves while another reads its part
   }
+  dec_status(a, sh, bits);
 }
 
 // fp32 on the CUDA cores, in packed pairs (two multiply-adds per instruction).
@@ -791,27 +942,15 @@ __device__ __forceinline__ int dec_heads_of(const DecodeArgs& a, const int4& j) 
   return min(kDecHeads, a.group - j.y % a.hgroups * kDecHeads);
 }
 
-// Status of the call: what the blocks of the first kernel saw. One warp.
-__device__ __forceinline__ void dec_collect(const DecodeArgs& a, int B) {
-  uint32_t v = 0;
-  for (int i = threadIdx.x & 31; i < B; i += 32) v |= (uint32_t)a.status[i];
-  v = __reduce_or_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) {
-    a.hdr->status = v;
-    a.hdr->detail = v ? 0x9100u : 0u;
-  }
-}
-
 // Joins the parts of runs that were cut; two forms, both for any number of parts.
 // Few parts: a block per entry of joins, a warp per head; the first parts' values
 // are on their way before the weights are known.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a, int B) {
+__global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a) {
   constexpr int E2 = D / 64, kEarly = 6;
   const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
   dependency_release();
   dependency_wait();
-  if (blockIdx.x == 0 && h == kDecHeads - 1) dec_collect(a, B);
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0 || h >= dec_heads_of(a, j)) return;
   const DecParts<D> p(a, j, h);
@@ -868,13 +1007,12 @@ __global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a
 // dependent loads, 3 us so).
 constexpr int kJoinThreads = 512;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_many_kernel(const DecodeArgs a, int B) {
+__global__ void __launch_bounds__(kJoinThreads) decode_join_many_kernel(const DecodeArgs a) {
   constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
   __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
   dependency_release();
   dependency_wait();
-  if (blockIdx.x == 0 && h == 0 && warp == W - 1) dec_collect(a, B);
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0 || h >= dec_heads_of(a, j)) return;
   const DecParts<D> p(a, j, h);
@@ -949,23 +1087,36 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   int64_t grid = S::kBlocks * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;
   if (grid > tiles) grid = tiles;
-  a.by_run = runs <= grid;
   a.in_page = a.cs.page_size % S::kKeys == 0;
   a.tile_pages = S::kTile / a.cs.page_size;
   a.tile_rest = S::kTile % a.cs.page_size;
+  // Few short runs: a cluster of blocks each, as many as the tables' longest run fills, with
+  // up to 4 tiles a block.
+  const int64_t run_tiles = dec_run_tiles(a.max_len, S::kTile);
+  for (int C = kDecCluster; C >= 1; C /= 2) {
+    if (run_tiles * 2 <= C || run_tiles > 4 * C || runs * C > S::kBlocks * (int64_t)sms ||
+        runs * C > kDecMaxBlocks)
+      continue;
+    const int rc = allow_smem(decode_cluster_kernel<M>, S::kSmem);
+    if (rc != ADASPARK_OK) return rc;
+    return cuda_status(launch_after("decode_attn", decode_cluster_kernel<M>,
+                                    dim3((unsigned)(runs * C)), dim3(kDecWarps * 32), S::kSmem, s,
+                                    C, a, C));
+  }
+  a.by_run = runs <= grid;
   int rc = allow_smem(decode_kernel<M>, S::kSmem);
   if (rc == ADASPARK_OK)
     rc = cuda_status(launch_after("decode_attn", decode_kernel<M>, dim3((unsigned)grid),
-                                  dim3(kDecWarps * 32), S::kSmem, s, a));
+                                  dim3(kDecWarps * 32), S::kSmem, s, 1, a));
   if (rc != ADASPARK_OK) return rc;
   // Parts per run, about: from some 16 on their loads go side by side in a block.
   const unsigned entries = (unsigned)(a.by_run ? runs : grid);
   if (grid / runs >= 16)
     return cuda_status(launch_after("decode_join", decode_join_many_kernel<typename S::T, S::D>,
                                     dim3(entries, a.group < kDecHeads ? a.group : kDecHeads),
-                                    dim3(kJoinThreads), 0, s, a, (int)grid));
+                                    dim3(kJoinThreads), 0, s, 1, a));
   return cuda_status(launch_after("decode_join", decode_join_few_kernel<typename S::T, S::D>,
-                                  dim3(entries), dim3(32 * kDecHeads), 0, s, a, (int)grid));
+                                  dim3(entries), dim3(32 * kDecHeads), 0, s, 1, a));
 }
 
 }  // namespace

@@ -40,20 +40,22 @@ inline int allow_smem(void (*kernel)(KArgs...), int bytes) {
 
 // launch() of a kernel whose blocks may come up while the stream's previous
 // kernel still runs: it must call dependency_wait() (common.cuh) before it
-// touches anything that kernel writes.
+// touches anything that kernel writes. `cluster`: blocks per cluster along x.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_after(const char* name, void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                size_t smem, cudaStream_t s, Args&&... args) {
+                                size_t smem, cudaStream_t s, int cluster, Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   timer_begin(name, s);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
   if (e == cudaSuccess) e = cudaGetLastError();

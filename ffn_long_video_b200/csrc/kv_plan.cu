@@ -146,6 +146,7 @@ __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* s
     if (ok) *a.n_free = (int32_t)left;   // every thread has read it
     a.hdr->status = ok ? 0u : sound ? ADASPARK_DEV_PAGES : ADASPARK_DEV_BAD_LAYOUT;
     a.hdr->detail = ok ? 0u : 0x8100u;
+    a.hdr->n_block_status = 0;
   }
   return t;
 }
@@ -356,15 +357,15 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   a.div_shift = 31 + k;
   a.div_mul = (uint32_t)((((uint64_t)1 << (31 + k)) + page_size - 1) / page_size);
   if (n_rows <= kPlanOneBlock && n_seqs <= kPlanSeqs)
-    return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a));
+    return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a));
   cudaError_t e =
-      launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+      launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
   if (e == cudaSuccess) {
     const int64_t want = ((int64_t)n_rows + 4095) / 4096;  // 128 rows a warp
     const int64_t most = (int64_t)sms * 2;
     const unsigned grid = (unsigned)(want < most ? want : most);
     e = launch_after("kv_plan_write", plan_write_kernel, dim3(grid), dim3(kPlanThreads), 0,
-                     s, a);
+                     s, 1, a);
   }
   return cuda_status(e);
 }

@@ -632,12 +632,12 @@ cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
                                     : rope_walk_kernel<T, D, false, CACHE, NORM, true>)
                               : (il ? rope_walk_kernel<T, D, true, CACHE, NORM, false>
                                     : rope_walk_kernel<T, D, false, CACHE, NORM, false>);
-    return launch_after(name, kernel, grid, block, 0, s, a);
+    return launch_after(name, kernel, grid, block, 0, s, 1, a);
   }
   if (n * steps > INT32_MAX - 3) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((n * steps + 3) / 4));
-  return il ? launch_after(name, rope_step_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, a)
-            : launch_after(name, rope_step_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, a);
+  return il ? launch_after(name, rope_step_kernel<T, D, true, CACHE, NORM>, grid, block, 0, s, 1, a)
+            : launch_after(name, rope_step_kernel<T, D, false, CACHE, NORM>, grid, block, 0, s, 1, a);
 }
 
 template <typename T, int D, bool CACHE>
@@ -667,9 +667,9 @@ template <typename T, typename T2, int D, bool NORM>
 cudaError_t launch_bwd(const BwdCall& b, bool il, cudaStream_t s) {
   const dim3 grid(b.blocks), block(128);
   if (il)
-    return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, true, NORM>, grid, block, 0, s, b.a,
+    return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, true, NORM>, grid, block, 0, s, 1, b.a,
                   b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
-  return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, false, NORM>, grid, block, 0, s, b.a,
+  return launch_after("qk_rope_backward", rope_bwd_kernel<T, T2, D, false, NORM>, grid, block, 0, s, 1, b.a,
                 b.dq, b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
 }
 
@@ -873,7 +873,7 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     e = dy_dtype == ADASPARK_BF16 ? dispatch_bwd<float, bf16>(b, d, il, s)
                                   : dispatch_bwd<float, float>(b, d, il, s);
   if (e == cudaSuccess && norm)
-    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 8), dim3(1024), 0, s, b.part, blocks, d,
+    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 8), dim3(1024), 0, s, 1, b.part, blocks, d,
                w_q ? dw_q : nullptr, w_k ? dw_k : nullptr);
   return cuda_status(e);
 }

@@ -103,9 +103,28 @@ LENS = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 300, 0, 513]
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("hq,hkv,d", [(28, 4, 128), (16, 2, 128), (4, 1, 64), (6, 3, 64), (3, 3, 128),
                                       (16, 1, 128), (9, 1, 64), (24, 2, 128)])
-def test_lengths_and_heads(hq, hkv, d, dtype):
-    case = _make(LENS, hq, hkv, d, dtype, 16, seed=hq)
+@pytest.mark.parametrize("spare_cols", [0, 3000])
+def test_lengths_and_heads(hq, hkv, d, dtype, spare_cols):
+    """Tables as long as the longest sequence (a cluster of blocks per run), and
+    far longer ones (the line of tiles over the GPU)."""
+    case = _make(LENS, hq, hkv, d, dtype, 16, seed=hq, spare_cols=spare_cols)
     _check(*case, *_run(*case))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n_seqs,longest", [(1, 1), (1, 64), (1, 65), (2, 129), (1, 500), (5, 256),
+                                            (3, 1000), (1, 2048), (1, 2049), (60, 70), (100, 33)])
+def test_few_short_sequences(n_seqs, longest, dtype):
+    """Clusters of 1 to 8 blocks per run and their borders: runs of one tile to
+    four a block, blocks without a tile, sequences without keys."""
+    r = np.random.default_rng(longest)
+    lens = r.integers(0, longest + 1, n_seqs)
+    lens[-1] = longest
+    case = _make(lens, 7, 1, 128, dtype, 16, seed=longest)
+    out, lse = _run(*case)
+    _check(*case, out, lse)
+    o, l = _run(*case)
+    assert torch.equal(o, out) and torch.equal(l, lse)
 
 
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (FP32, 128), (FP32, 64)])
@@ -151,8 +170,9 @@ def test_all_sequences_empty():
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
-def test_scales(scale):
-    case = _make([100, 7], 8, 2, 64, FP32, 16, seed=4)
+@pytest.mark.parametrize("spare_cols", [0, 3000])
+def test_scales(scale, spare_cols):
+    case = _make([100, 7], 8, 2, 64, FP32, 16, seed=4, spare_cols=spare_cols)
     _check(*case, *_run(*case, scale=scale), scale=scale)
 
 
@@ -166,10 +186,12 @@ def test_large_scores(dtype):
     _check(q, k, v, table, lens, *_run(q, k, v, table, lens))
 
 
-def test_infinite_scores():
+@pytest.mark.parametrize("spare_cols", [0, 3000])
+def test_infinite_scores(spare_cols):
     """Every score -inf: nothing is left of the row (0, -inf).  Some: those keys
     weigh nothing.  A NaN or +inf score makes its row NaN and no other."""
-    q, k, v, table, lens = _make([40, 40, 40, 40], 4, 4, 64, FP32, 8, seed=6, garbage=False)
+    q, k, v, table, lens = _make([40, 40, 40, 40], 4, 4, 64, FP32, 8, seed=6, garbage=False,
+                                 spare_cols=spare_cols)
     q.fill_(1.0)
     # key j of sequence i on its page, head i only
     def key(i, j):
@@ -210,10 +232,11 @@ def test_strides_and_given_outputs():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
-def test_bad_lengths_and_pages_are_flagged():
+@pytest.mark.parametrize("spare_cols", [0, 3000])
+def test_bad_lengths_and_pages_are_flagged(spare_cols):
     """A length the table cannot hold counts as 0, a page that is not there holds
     no keys; both are reported, and other sequences are as without them."""
-    case = _make([40, 60, 50], 8, 2, 128, BF16, 16, seed=8)
+    case = _make([40, 60, 50], 8, 2, 128, BF16, 16, seed=8, spare_cols=spare_cols)
     q, k, v, table, lens = case
     want = _run(*case)
     for bad in (-1, table.shape[1] * 16 + 1, 2 ** 31 - 1, -2 ** 31):
