@@ -13,6 +13,8 @@
 // Latency-bound: one block sums the sequences' takes, gifts and new tokens and, for
 // a step's few rows, writes slots, table and list entries as well; for many rows
 // (prompts) a second kernel writes them over the whole GPU.
+#include <algorithm>
+
 #include "serve.h"
 
 namespace adaspark {
@@ -63,87 +65,113 @@ __device__ __forceinline__ int plan_pages(const PlanArgs& a, int n) {
 }
 
 // Inclusive sums of three values over the warp.
-__device__ __forceinline__ void warp_scan3(long long (&v)[3]) {
+template <typename I>
+__device__ __forceinline__ void warp_scan3(I (&v)[3]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const long long u = __shfl_up_sync(0xffffffffu, v[k], o);
+      const I u = __shfl_up_sync(0xffffffffu, v[k], o);
       if (lane >= o) v[k] += u;
     }
   }
 }
 
-// Sums over the sequences (one block), the plan's check, its totals; n_free and the
-// status are written here. keep: the sums stay in shared memory (n_seqs <= kPlanSeqs),
-// else they go to the workspace.
+// Sums over the sequences (one block of whole warps), the plan's check, its totals;
+// n_free and the status are written here. KEEP: the sums stay in shared memory
+// (n_seqs <= kPlanSeqs), else they go to the workspace.
+constexpr int kPlanTooMuch = 1 << 21;  // 1024 values below it sum up in 31 bits
 template <bool KEEP>
 __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* sh) {
-  __shared__ long long warp_sum[2][kPlanThreads / 32][3];
-  __shared__ int bad;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int warp_sum[2][kPlanThreads / 32][3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const long long F = *a.n_free;
-  if (threadIdx.x == 0) bad = 0;
-  __syncthreads();
   const long long most = (long long)a.max_pages * a.page_size;
   long long carry[3] = {0, 0, 0};
-  for (int base = 0, buf = 0; base < a.n_seqs; base += kPlanThreads, buf ^= 1) {
+  bool bad = false;
+  for (int base = 0, buf = 0; base < a.n_seqs; base += blockDim.x, buf ^= 1) {
     const int i = base + threadIdx.x;
-    long long own[3] = {0, 0, 0};
+    int o = 0, n = 0;
     if (i < a.n_seqs) {
-      const int o = a.old_lens[i], n = a.new_lens[i];
+      o = a.old_lens[i];
+      n = a.new_lens[i];
       if (KEEP) {
         sh->old_lens[i] = o;
         sh->new_lens[i] = n;
       }
-      if (o < 0 || n < 0 || o > most || n > most) {
-        bad = 1;
-      } else {
-        const int po = plan_pages(a, o), pn = plan_pages(a, n);
-        own[0] = max(pn - po, 0);
-        own[1] = max(po - pn, 0);
-        own[2] = max(n - o, 0);
+    }
+    const bool wrong = o < 0 || n < 0 || o > most || n > most;
+    if (wrong) o = n = 0;
+    const int po = plan_pages(a, o), pn = plan_pages(a, n);
+    const int own[3] = {max(pn - po, 0), max(po - pn, 0), max(n - o, 0)};
+    // sums of this round in 32 bits where they fit, which one barrier tells; else in 64
+    const bool large = max(max(own[0], own[1]), own[2]) >= kPlanTooMuch;
+    bad |= wrong;
+    long long before[3], total[3];
+    if (!__syncthreads_or(large)) {
+      int v[3] = {own[0], own[1], own[2]};
+      warp_scan3(v);
+      if (lane == 31) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) warp_sum[buf][warp][k] = v[k];
       }
-    }
-    long long v[3] = {own[0], own[1], own[2]};
-    warp_scan3(v);
-    if (lane == 31) {
+      __syncthreads();
+      // every warp sums the warps' totals
+      int w[3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) warp_sum[buf][warp][k] = v[k];
-    }
-    __syncthreads();
-    // every warp sums the warps' totals
-    long long w[3];
+      for (int k = 0; k < 3; ++k) w[k] = lane < warps ? warp_sum[buf][lane][k] : 0;
+      warp_scan3(w);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) w[k] = warp_sum[buf][lane][k];
-    warp_scan3(w);
+      for (int k = 0; k < 3; ++k) {
+        const int up = __shfl_sync(0xffffffffu, w[k], max(warp - 1, 0));
+        before[k] = v[k] - own[k] + (warp ? up : 0);
+        total[k] = __shfl_sync(0xffffffffu, w[k], 31);
+      }
+    } else {
+      __shared__ long long wide[kPlanThreads / 32][3];
+      long long v[3] = {own[0], own[1], own[2]};
+      warp_scan3(v);
+      __syncthreads();
+      if (lane == 31) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const long long before = __shfl_sync(0xffffffffu, w[k], max(warp - 1, 0));
-      v[k] += carry[k] + (warp ? before : 0) - own[k];
-      carry[k] += __shfl_sync(0xffffffffu, w[k], 31);
+        for (int k = 0; k < 3; ++k) wide[warp][k] = v[k];
+      }
+      __syncthreads();
+      long long w[3];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) w[k] = lane < warps ? wide[lane][k] : 0;
+      warp_scan3(w);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const long long up = __shfl_sync(0xffffffffu, w[k], max(warp - 1, 0));
+        before[k] = v[k] - own[k] + (warp ? up : 0);
+        total[k] = __shfl_sync(0xffffffffu, w[k], 31);
+      }
     }
     if (i < a.n_seqs) {
       // sums of a plan that holds fit 31 bits; another's are not used
-      (KEEP ? sh->take0 : a.take0)[i] = (int32_t)v[0];
-      (KEEP ? sh->give0 : a.give0)[i] = (int32_t)v[1];
-      if (KEEP) sh->starts[i] = (int32_t)v[2];
-      a.starts[i] = (int32_t)v[2];
+      (KEEP ? sh->take0 : a.take0)[i] = (int32_t)(carry[0] + before[0]);
+      (KEEP ? sh->give0 : a.give0)[i] = (int32_t)(carry[1] + before[1]);
+      if (KEEP) sh->starts[i] = (int32_t)(carry[2] + before[2]);
+      a.starts[i] = (int32_t)(carry[2] + before[2]);
     }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) carry[k] += total[k];
   }
-  __syncthreads();
+  // n_free was read, the sums are there
+  const bool any_bad = __syncthreads_or(bad);
   const long long left = F + carry[1] - carry[0];
   // lengths the tables hold, rows for every new token, no more pages than there are
-  const bool sound = !bad && carry[2] <= a.n_rows && F >= 0 && F <= a.n_pages &&
+  const bool sound = !any_bad && carry[2] <= a.n_rows && F >= 0 && F <= a.n_pages &&
                      carry[1] <= a.n_pages && left <= a.n_pages;
   const bool ok = sound && left >= 0;
   if (!ok)
-    for (int i = threadIdx.x; i < a.n_seqs; i += kPlanThreads) a.starts[i] = 0;
+    for (int i = threadIdx.x; i < a.n_seqs; i += blockDim.x) a.starts[i] = 0;
   const PlanTotals t{ok, (int32_t)carry[2], (int32_t)carry[0], (int32_t)carry[1], (int32_t)F};
   if (threadIdx.x == 0) {
     a.starts[a.n_seqs] = ok ? t.rows : 0;
-    if (ok) *a.n_free = (int32_t)left;   // every thread has read it
+    if (ok) *a.n_free = (int32_t)left;
     a.hdr->status = ok ? 0u : sound ? ADASPARK_DEV_PAGES : ADASPARK_DEV_BAD_LAYOUT;
     a.hdr->detail = ok ? 0u : 0x8100u;
     a.hdr->n_block_status = 0;
@@ -275,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   const PlanTotals t = plan_sums<true>(a, &sh);
   __syncthreads();   // the status is there for plan_write's flags
   plan_write(a, {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts}, t, threadIdx.x >> 5,
-             kPlanThreads / 32);
+             blockDim.x >> 5);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs a) {
@@ -356,8 +384,11 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   while ((int64_t)1 << k < page_size) ++k;
   a.div_shift = 31 + k;
   a.div_mul = (uint32_t)((((uint64_t)1 << (31 + k)) + page_size - 1) / page_size);
-  if (n_rows <= kPlanOneBlock && n_seqs <= kPlanSeqs)
-    return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a));
+  if (n_rows <= kPlanOneBlock && n_seqs <= kPlanSeqs) {
+    // no more warps than sequences and rows give work
+    const int threads = std::min(kPlanThreads, (std::max(n_seqs, n_rows) + 127) / 128 * 128);
+    return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(threads), 0, s, 1, a));
+  }
   cudaError_t e =
       launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
   if (e == cudaSuccess) {

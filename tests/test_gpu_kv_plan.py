@@ -131,6 +131,14 @@ def test_long_prompts_and_a_million_rows():
     st.step(np.where(np.arange(n) % 2 == 0, 65536, 0), n * 65536)
 
 
+def test_prompts_of_millions():
+    """New tokens of one sequence past 2^21: sums in 64 bits."""
+    st = State(3, 50000, 64, 60000)
+    st.step([2 ** 21 + 5, 100, 0], 2 ** 21 + 200)
+    st.step([2 ** 21 + 6, 0, 130], 300)
+    st.step([0, 7, 2 ** 21], 2 ** 21 + 7)
+
+
 def test_captured_steps_share_a_workspace():
     """Two captured steps over one pool and one workspace, replayed in turn, act
     as the same steps run one by one."""
