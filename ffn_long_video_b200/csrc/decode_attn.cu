@@ -13,6 +13,7 @@
 // leaves partial results in the workspace (at most two per block), and a second
 // kernel joins them. The cut follows lengths and grid alone, and parts are joined
 // in order, so results do not depend on timing.
+#include <algorithm>
 #include <cmath>
 
 #include "serve.h"
@@ -37,7 +38,7 @@ struct DecodeArgs {
   void* out;
   float* lse;                    // or null
   float scale_log2;              // scale * log2(e)
-  int32_t n_seqs, max_len, hq, hkv, group, hgroups;  // hgroups: groups of 8 heads per KV head
+  int32_t n_seqs, max_len, hq, hkv, group, hgroups;  // hgroups: runs per KV head
   int32_t by_run;
   int32_t in_page;               // a page holds a whole number of stages
   int32_t tile_pages, tile_rest; // pages and tokens beyond them that a tile spans
@@ -45,10 +46,10 @@ struct DecodeArgs {
   int4* joins;                   // {seq, KV head * hgroups + group, first slot, last slot} or -1:
                                  // of each run (by_run: there are no more than blocks), or of
                                  // the cut run that starts in each block
-  float* part;                   // [2 grid][8][D + 2]: outputs, maximum (log2), sum
+  float* part;                   // [2 grid][H][D + 2]: outputs, maximum (log2), sum
 };
 
-constexpr int kDecHeads = 8;     // query heads of a run
+constexpr int kDecMaxHeads = 16;
 constexpr int kDecWarps = 4;
 constexpr int kDecMaxBlocks = 148 * 3;
 constexpr int kDecCluster = 8;   // blocks that join through shared memory, at most
@@ -69,16 +70,19 @@ __device__ __forceinline__ void cp_async_wait() {
 // Sizes of a warp's work: a tile is kKeys keys of each of the block's warps, a
 // stage a warp's share of it, a ring the stages it has in flight. bf16 rows are
 // padded so that the 8 rows of a matrix load fall on different banks.
-template <typename T_, int D_>
+template <typename T_, int D_, int H_>
 struct DecShape {
   using T = T_;
-  static constexpr int D = D_;
+  static constexpr int D = D_, H = H_;                        // H: query heads of a run
   static constexpr int kKeys = 4096 / (D * (int)sizeof(T));  // 4 KB of K
   static constexpr int kTile = kKeys * kDecWarps;
   static constexpr int kRow = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 0);
   static constexpr int kStage = 2 * kKeys * kRow;            // K rows, V rows
   static constexpr int kStages = 2;
-  static constexpr int kBlocks = sizeof(T) == 2 ? 2 : 3;     // blocks per SM
+  // Blocks per SM (registers and shared memory allow no more): fp32 with 8 heads 2, with
+  // fewer 3 (30 sequences up to 12829 keys, 6 heads on 3: 52 us at 3, 67 at 2), bf16 with up
+  // to 8 heads 3, with 16 2.
+  static constexpr int kBlocks = (sizeof(T) == 2) == (H == 8) ? 3 : 2;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kSmem = kDecWarps * kRing;
   static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
@@ -108,7 +112,7 @@ struct DecLine {
 struct DecShared {
   int warp_sum[kDecWarps];
   DecSpot first;
-  float m[kDecWarps][kDecHeads], l[kDecWarps][kDecHeads];
+  float m[kDecWarps][kDecMaxHeads], l[kDecWarps][kDecMaxHeads];
   uint32_t bits[kDecWarps];
 };
 
@@ -325,11 +329,11 @@ __device__ __forceinline__ void dec_end_run(const DecodeArgs& a, DecShared& sh, 
   using S = typename M::S;
   using T = typename S::T;
   constexpr int D = S::D, E = D / 32;
-  static_assert(kDecHeads * (D + 4) * 4 <= S::kStage, "");
+  static_assert(S::H * (D + 4) * 4 <= S::kStage, "");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
-  const int heads = min(kDecHeads, a.group - hg * kDecHeads);
-  const int h0 = kvh * a.group + hg * kDecHeads;
+  const int heads = min(S::H, a.group - hg * S::H);
+  const int h0 = kvh * a.group + hg * S::H;
   const bool whole = from == 0 && at.tile + 1 == at.tiles;
   const int slot = 2 * blockIdx.x + (u == L.u0 ? 0 : 1);
   math.sums(sh.m[warp], sh.l[warp]);
@@ -359,7 +363,7 @@ __device__ __forceinline__ void dec_end_run(const DecodeArgs& a, DecShared& sh, 
             from_f32<T>(ll == 0.f ? 0.f : acc[e] * r);
       if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     } else {
-      float* pp = a.part + ((int64_t)slot * kDecHeads + h) * (D + 2);
+      float* pp = a.part + ((int64_t)slot * S::H + h) * (D + 2);
 #pragma unroll
       for (int e = 0; e < E; ++e) pp[32 * e + lane] = acc[e];
       if (lane == 0) {
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ DecShared sh;
   __shared__ typename M::Shared msh;
-  __shared__ float part[kDecHeads][D + 2];   // this block's outputs, maxima, sums
+  __shared__ float part[S::H][D + 2];   // this block's outputs, maxima, sums
   dependency_release();
   dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -488,9 +492,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
   at.run = blockIdx.x / C - at.seq * runs;
   at.len = dec_len(a, at.seq, &bits);
   at.tiles = (at.len + S::kTile - 1) / S::kTile;
-  const int heads = min(kDecHeads, a.group - at.run % a.hgroups * kDecHeads);
+  const int heads = min(S::H, a.group - at.run % a.hgroups * S::H);
   const int64_t row0 = (int64_t)at.seq * a.hq + at.run / a.hgroups * a.group +
-                       at.run % a.hgroups * kDecHeads;
+                       at.run % a.hgroups * S::H;
   if (at.len == 0) {
     if (rank == 0) {
       for (int e = threadIdx.x; e < heads * D; e += kDecWarps * 32)
@@ -592,23 +596,25 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
 // fp32 on the CUDA cores, in packed pairs (two multiply-adds per instruction).
 // Scores: 8 lanes share a key (16 or 8 elements each, queries from shared memory,
 // two keys at a time), 4 keys side by side; 7 exchanges leave lane j of them with
-// head j. Outputs: a lane holds D / 32 elements of 8 heads. Weights pass through
+// head j (H = 2 or 4 heads: of them once or twice more). Outputs: a lane holds D / 32 elements of 8 heads. Weights pass through
 // shared memory, written twice as a pair so that they load as one. Outputs and
 // sums are kept in two levels (kFlush tiles, then all): one chain of 2400 keys
-// had twice the error.
-template <int D>
+// had twice the error. 24 sequences of 20000 to 30001 keys, 28 heads on 4: 390 us
+// (floor 384) while the clocks hold; back to back the power limit lowers them and
+// it takes 455 to 485.
+template <int D, int H>
 struct DecFp32 {
-  using S = DecShape<float, D>;
+  using S = DecShape<float, D, H>;
   static constexpr int E2 = D / 64, KK = S::kKeys, kFlush = 8;
   struct Shared {
-    __align__(16) float q[kDecHeads][D];
-    __align__(16) float2 p[kDecWarps][KK][kDecHeads];
+    __align__(16) float q[H][D];
+    __align__(16) float2 p[kDecWarps][KK][H];
   };
   const DecodeArgs& a;
   Shared& sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kg = lane >> 3, j = lane & 7;
-  F2 o[kDecHeads][E2], om[kDecHeads][E2];
-  float m, l, lm;  // this lane's head: j
+  F2 o[H][E2], om[H][E2];
+  float m, l, lm;  // this lane's head: j % H
   int n;
 
   __device__ __forceinline__ DecFp32(const DecodeArgs& a_, Shared& sh_) : a(a_), sh(sh_) {}
@@ -622,14 +628,14 @@ struct DecFp32 {
   // All threads, at a point where no warp reads the queries of the run before.
   __device__ __forceinline__ void begin(const DecSpot& at) {
     const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
-    const int heads = min(kDecHeads, a.group - hg * kDecHeads);
+    const int heads = min(H, a.group - hg * H);
     const float* q = static_cast<const float*>(a.q) + at.seq * a.qs.ts +
-                     (int64_t)(kvh * a.group + hg * kDecHeads) * a.qs.hs;
-    for (int e = threadIdx.x; e < kDecHeads * D; e += kDecWarps * 32)
+                     (int64_t)(kvh * a.group + hg * H) * a.qs.hs;
+    for (int e = threadIdx.x; e < H * D; e += kDecWarps * 32)
       sh.q[e / D][e % D] = e / D < heads ? q[e / D * a.qs.hs + e % D] : 0.f;
     __syncthreads();
 #pragma unroll
-    for (int h = 0; h < kDecHeads; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int e = 0; e < E2; ++e) o[h][e] = om[h][e] = f2(0.f, 0.f);
     m = -INFINITY;
@@ -638,20 +644,20 @@ struct DecFp32 {
   }
 
   __device__ __forceinline__ void tile(const uint8_t* st, uint32_t here) {
-    float z[KK / 4];  // of key 4 g + kg and head j
+    float z[KK / 4];  // of key 4 g + kg and head j % H
     float top = -INFINITY;
 #pragma unroll
     for (int g = 0; g < KK / 4; g += 2) {
-      F2 acc[2][kDecHeads];
+      F2 acc[2][H];
 #pragma unroll
-      for (int h = 0; h < kDecHeads; ++h) acc[0][h] = acc[1][h] = f2(0.f, 0.f);
+      for (int h = 0; h < H; ++h) acc[0][h] = acc[1][h] = f2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         F2 ka, kb, kc, kd;
         lds(st + (4 * g + kg) * S::kRow + 16 * (j + 8 * c), ka, kb);
         lds(st + (4 * g + 4 + kg) * S::kRow + 16 * (j + 8 * c), kc, kd);
 #pragma unroll
-        for (int h = 0; h < kDecHeads; ++h) {
+        for (int h = 0; h < H; ++h) {
           F2 qa, qb;
           lds(&sh.q[h][4 * (j + 8 * c)], qa, qb);
           acc[0][h] = fma2(ka, qa, acc[0][h]);
@@ -662,20 +668,26 @@ struct DecFp32 {
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float d[kDecHeads];
+        float d[H];
 #pragma unroll
-        for (int h = 0; h < kDecHeads; ++h) {
+        for (int h = 0; h < H; ++h) {
           const float2 v = unpack(acc[x][h]);
           d[h] = v.x + v.y;
         }
-        // halve the values while folding the lanes: lane bit w keeps the half with that bit
+        // fold the lanes, halving the values while there are more than one: lane bit w keeps
+        // the half with that bit
 #pragma unroll
         for (int w = 4; w >= 1; w >>= 1) {
+          if (w >= H) {
 #pragma unroll
-          for (int k = 0; k < w; ++k) {
-            const bool up = lane & w;
-            const float keep = up ? d[k + w] : d[k], give = up ? d[k] : d[k + w];
-            d[k] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+            for (int k = 0; k < H; ++k) d[k] += __shfl_xor_sync(0xffffffffu, d[k], w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < w; ++k) {
+              const bool up = lane & w;
+              const float keep = up ? d[k + w] : d[k], give = up ? d[k] : d[k + w];
+              d[k] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+            }
           }
         }
         const bool ok = here >> (4 * (g + x) + kg) & 1;
@@ -693,7 +705,7 @@ struct DecFp32 {
       l *= alpha;
       lm *= alpha;
 #pragma unroll
-      for (int h = 0; h < kDecHeads; ++h) {
+      for (int h = 0; h < H; ++h) {
         const float f = __shfl_sync(0xffffffffu, alpha, h);
         const F2 ff = f2(f, f);
 #pragma unroll
@@ -707,7 +719,7 @@ struct DecFp32 {
     for (int g = 0; g < KK / 4; ++g) {
       const float p = exp2f(z[g] - m_use);
       l += p;
-      sh.p[warp][4 * g + kg][j] = make_float2(p, p);
+      if (j < H) sh.p[warp][4 * g + kg][j] = make_float2(p, p);
     }
     __syncwarp();
 #pragma unroll
@@ -719,7 +731,7 @@ struct DecFp32 {
       else
         x[0].v = *reinterpret_cast<const unsigned long long*>(row);
 #pragma unroll
-      for (int h = 0; h < kDecHeads; h += 2) {
+      for (int h = 0; h < H; h += 2) {
         F2 pa, pb;
         lds(&sh.p[warp][k][h], pa, pb);
 #pragma unroll
@@ -737,7 +749,7 @@ struct DecFp32 {
     lm += l;
     l = 0.f;
 #pragma unroll
-    for (int h = 0; h < kDecHeads; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int e = 0; e < E2; ++e) {
         om[h][e] = add2(om[h][e], o[h][e]);
@@ -745,18 +757,18 @@ struct DecFp32 {
       }
   }
 
-  __device__ __forceinline__ void sums(float (&ms)[kDecHeads], float (&ls)[kDecHeads]) {
+  __device__ __forceinline__ void sums(float* ms, float* ls) {
     flush();
     lm += __shfl_xor_sync(0xffffffffu, lm, 8);
     lm += __shfl_xor_sync(0xffffffffu, lm, 16);
-    if (lane < kDecHeads) {
+    if (lane < H) {
       ms[lane] = m;
       ls[lane] = lm;
     }
   }
   __device__ __forceinline__ void outputs(float* out) const {
 #pragma unroll
-    for (int h = 0; h < kDecHeads; ++h)
+    for (int h = 0; h < H; ++h)
 #pragma unroll
       for (int e = 0; e < E2; ++e)
         *reinterpret_cast<float2*>(&out[h * (D + 4) + lane * 2 * E2 + 2 * e]) = unpack(om[h][e]);
@@ -789,140 +801,166 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// bf16: keys fill the rows of a product's tile and 8 query heads its columns,
+// bf16: keys fill the rows of a product's tile and query heads its columns,
 //   S^T [16 keys x 8 heads] = K Q^T,   O^T [16 d x 8 heads] += V^T P^T,
 // so that no part of a tile is padding when a KV head serves 8 query heads (the
 // 128 rows of a tcgen05 tile would hold 7 or 8 of them), and a lane's softmax
-// columns are its output columns. P goes to the second product as two bf16 parts
-// (high and rest: 2^-17 relative), which costs 8 more products per 16 keys and
-// keeps the output as near as fp32 weights would.
-template <int D>
+// columns are its output columns. NT = 2: up to 16 heads, each load of a key feeds
+// two products. P goes to the second product as two bf16 parts (high and rest:
+// 2^-17 relative), which costs 8 more products per 16 keys and keeps the output as
+// near as fp32 weights would.
+template <int D, int NT>
 struct DecBf16 {
-  using S = DecShape<__nv_bfloat16, D>;
+  using S = DecShape<__nv_bfloat16, D, 8 * NT>;
   static constexpr int KK = S::kKeys, MT = KK / 16, DT = D / 16;
   struct Shared {};
   const DecodeArgs& a;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  uint32_t qf[DT][2];
-  float o[DT][4];
-  float m0, m1, l0, l1;  // heads 2c, 2c + 1
+  uint32_t qf[NT][DT][2];
+  float o[NT][DT][4];
+  float m[NT][2], l[NT][2];  // heads 8 n + 2c, 2c + 1
 
   __device__ __forceinline__ DecBf16(const DecodeArgs& a_, Shared&) : a(a_) {}
 
   __device__ __forceinline__ void begin(const DecSpot& at) {
     const int kvh = at.run / a.hgroups, hg = at.run % a.hgroups;
-    const int heads = min(kDecHeads, a.group - hg * kDecHeads);
+    const int heads = min(S::H, a.group - hg * S::H);
     // Q^T: column g is head g, rows 2c, 2c + 1 and 8 further of each 16 of d
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + at.seq * a.qs.ts +
-                             (int64_t)(kvh * a.group + hg * kDecHeads + g) * a.qs.hs + 2 * c;
+                             (int64_t)(kvh * a.group + hg * S::H + g) * a.qs.hs + 2 * c;
 #pragma unroll
-    for (int k = 0; k < DT; ++k) {
-      qf[k][0] = g < heads ? *reinterpret_cast<const uint32_t*>(q + 16 * k) : 0u;
-      qf[k][1] = g < heads ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8) : 0u;
+    for (int n = 0; n < NT; ++n) {
+      const bool there = 8 * n + g < heads;
+      const __nv_bfloat16* p = q + (int64_t)8 * n * a.qs.hs;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
+      for (int k = 0; k < DT; ++k) {
+        qf[n][k][0] = there ? *reinterpret_cast<const uint32_t*>(p + 16 * k) : 0u;
+        qf[n][k][1] = there ? *reinterpret_cast<const uint32_t*>(p + 16 * k + 8) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][k][e] = 0.f;
+      }
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
     }
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
   }
 
   __device__ __forceinline__ void tile(const uint8_t* st, uint32_t here) {
-    // scores: rows g and g + 8 of each 16 keys, heads 2c and 2c + 1
-    float z[MT][4];
-    float t0 = -INFINITY, t1 = -INFINITY;
+    // scores: rows g and g + 8 of each 16 keys, heads 2c and 2c + 1 of each 8
+    float z[NT][MT][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      float s0[4] = {}, s1[4] = {};  // even and odd steps: two shorter chains
+      float s0[NT][4] = {}, s1[NT][4] = {};  // even and odd steps: two shorter chains
       const uint8_t* row = st + (16 * t + (lane & 15)) * S::kRow + (lane >> 4) * 16;
 #pragma unroll
       for (int k = 0; k < DT; ++k) {
         uint32_t f[4];
         ldmatrix4(f, row + k * 32);
-        if (k & 1)
-          mma_16816(s1, f, qf[k][0], qf[k][1]);
-        else
-          mma_16816(s0, f, qf[k][0], qf[k][1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_16816(k & 1 ? s1[n] : s0[n], f, qf[n][k][0], qf[n][k][1]);
       }
       const bool lo = here >> (16 * t + g) & 1, hi = here >> (16 * t + g + 8) & 1;
-      z[t][0] = lo ? (s0[0] + s1[0]) * a.scale_log2 : -INFINITY;
-      z[t][1] = lo ? (s0[1] + s1[1]) * a.scale_log2 : -INFINITY;
-      z[t][2] = hi ? (s0[2] + s1[2]) * a.scale_log2 : -INFINITY;
-      z[t][3] = hi ? (s0[3] + s1[3]) * a.scale_log2 : -INFINITY;
-      t0 = fmaxf(t0, fmaxf(z[t][0], z[t][2]));
-      t1 = fmaxf(t1, fmaxf(z[t][1], z[t][3]));
-    }
 #pragma unroll
-    for (int w = 4; w <= 16; w <<= 1) {
-      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
-      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
-    }
-    t0 = fmaxf(t0, m0);
-    t1 = fmaxf(t1, m1);
-    const float u0 = t0 == -INFINITY ? 0.f : t0, u1 = t1 == -INFINITY ? 0.f : t1;
-    if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {
-      const float f0 = exp2f(m0 - u0), f1 = exp2f(m1 - u1);
-      l0 *= f0;
-      l1 *= f1;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < DT; ++k) {
-        o[k][0] *= f0; o[k][1] *= f1; o[k][2] *= f0; o[k][3] *= f1;
+        for (int e = 0; e < 4; ++e)
+          z[n][t][e] = (e < 2 ? lo : hi) ? (s0[n][e] + s1[n][e]) * a.scale_log2 : -INFINITY;
+    }
+    float use[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        t0 = fmaxf(t0, fmaxf(z[n][t][0], z[n][t][2]));
+        t1 = fmaxf(t1, fmaxf(z[n][t][1], z[n][t][3]));
       }
-      m0 = t0;
-      m1 = t1;
+#pragma unroll
+      for (int w = 4; w <= 16; w <<= 1) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, w));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, w));
+      }
+      t0 = fmaxf(t0, m[n][0]);
+      t1 = fmaxf(t1, m[n][1]);
+      use[n][0] = t0 == -INFINITY ? 0.f : t0;
+      use[n][1] = t1 == -INFINITY ? 0.f : t1;
+      if (__any_sync(0xffffffffu, t0 != m[n][0] || t1 != m[n][1])) {
+        const float f0 = exp2f(m[n][0] - use[n][0]), f1 = exp2f(m[n][1] - use[n][1]);
+        l[n][0] *= f0;
+        l[n][1] *= f1;
+#pragma unroll
+        for (int k = 0; k < DT; ++k) {
+          o[n][k][0] *= f0; o[n][k][1] *= f1; o[n][k][2] *= f0; o[n][k][3] *= f1;
+        }
+        m[n][0] = t0;
+        m[n][1] = t1;
+      }
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const float p0 = exp2f(z[t][0] - u0), p1 = exp2f(z[t][1] - u1);
-      const float p2 = exp2f(z[t][2] - u0), p3 = exp2f(z[t][3] - u1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      const uint32_t ha = pack_bf16x2(p0, p1), hb = pack_bf16x2(p2, p3);
-      const uint32_t ra = pack_bf16x2(p0 - __uint_as_float(ha << 16),
-                                      p1 - __uint_as_float(ha & 0xffff0000u));
-      const uint32_t rb = pack_bf16x2(p2 - __uint_as_float(hb << 16),
-                                      p3 - __uint_as_float(hb & 0xffff0000u));
-      const uint32_t ph0 = movmatrix(ha), ph1 = movmatrix(hb);
-      const uint32_t pr0 = movmatrix(ra), pr1 = movmatrix(rb);
+      uint32_t high[NT][2], rest[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float p0 = exp2f(z[n][t][0] - use[n][0]), p1 = exp2f(z[n][t][1] - use[n][1]);
+        const float p2 = exp2f(z[n][t][2] - use[n][0]), p3 = exp2f(z[n][t][3] - use[n][1]);
+        l[n][0] += p0 + p2;
+        l[n][1] += p1 + p3;
+        const uint32_t ha = pack_bf16x2(p0, p1), hb = pack_bf16x2(p2, p3);
+        const uint32_t ra = pack_bf16x2(p0 - __uint_as_float(ha << 16),
+                                        p1 - __uint_as_float(ha & 0xffff0000u));
+        const uint32_t rb = pack_bf16x2(p2 - __uint_as_float(hb << 16),
+                                        p3 - __uint_as_float(hb & 0xffff0000u));
+        high[n][0] = movmatrix(ha);
+        high[n][1] = movmatrix(hb);
+        rest[n][0] = movmatrix(ra);
+        rest[n][1] = movmatrix(rb);
+      }
       const uint8_t* row = st + (KK + 16 * t + (lane & 7) + (lane >> 4) * 8) * S::kRow +
                            (lane >> 3 & 1) * 16;
 #pragma unroll
       for (int k = 0; k < DT; ++k) {
         uint32_t f[4];
         ldmatrix4_trans(f, row + k * 32);
-        mma_16816(o[k], f, ph0, ph1);
-        mma_16816(o[k], f, pr0, pr1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_16816(o[n][k], f, high[n][0], high[n][1]);
+          mma_16816(o[n][k], f, rest[n][0], rest[n][1]);
+        }
       }
     }
   }
 
-  __device__ __forceinline__ void sums(float (&ms)[kDecHeads], float (&ls)[kDecHeads]) {
+  __device__ __forceinline__ void sums(float* ms, float* ls) {
 #pragma unroll
-    for (int w = 4; w <= 16; w <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, w);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, w);
-    }
-    if (g == 0) {
-      ms[2 * c] = m0;
-      ms[2 * c + 1] = m1;
-      ls[2 * c] = l0;
-      ls[2 * c + 1] = l1;
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], w);
+        if (g == 0) {
+          ms[8 * n + 2 * c + x] = m[n][x];
+          ls[8 * n + 2 * c + x] = l[n][x];
+        }
+      }
   }
   __device__ __forceinline__ void outputs(float* out) const {
 #pragma unroll
-    for (int k = 0; k < DT; ++k) {
-      float* p = out + 2 * c * (D + 4) + 16 * k + g;
-      p[0] = o[k][0];
-      p[D + 4] = o[k][1];
-      p[8] = o[k][2];
-      p[D + 12] = o[k][3];
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < DT; ++k) {
+        float* p = out + (8 * n + 2 * c) * (D + 4) + 16 * k + g;
+        p[0] = o[n][k][0];
+        p[D + 4] = o[n][k][1];
+        p[8] = o[n][k][2];
+        p[D + 12] = o[n][k][3];
+      }
   }
 };
 
 // A cut run's parts for one head, and where its results go.
-template <int D>
+template <class S>
 struct DecParts {
+  static constexpr int D = S::D;
   int n, first, rest;    // parts; slot of the first, then rest + 2 i
   const float* part;
   int64_t row;
@@ -932,36 +970,41 @@ struct DecParts {
     first = j.z;
     rest = j.z & ~1;
     part = a.part + (int64_t)h * (D + 2);
-    row = (int64_t)j.x * a.hq + j.y / a.hgroups * a.group + j.y % a.hgroups * kDecHeads + h;
+    row = (int64_t)j.x * a.hq + j.y / a.hgroups * a.group + j.y % a.hgroups * S::H + h;
   }
   __device__ __forceinline__ const float* operator[](int i) const {
-    return part + (int64_t)(i == 0 ? first : rest + 2 * i) * (kDecHeads * (D + 2));
+    return part + (int64_t)(i == 0 ? first : rest + 2 * i) * (S::H * (D + 2));
   }
 };
+template <class S>
 __device__ __forceinline__ int dec_heads_of(const DecodeArgs& a, const int4& j) {
-  return min(kDecHeads, a.group - j.y % a.hgroups * kDecHeads);
+  return min(S::H, a.group - j.y % a.hgroups * S::H);
 }
 
 // Joins the parts of runs that were cut; two forms, both for any number of parts.
-// Few parts: a block per entry of joins, a warp per head; the first parts' values
+// Few parts: a block per entry of joins, a warp per head; the first 8 parts' values
 // are on their way before the weights are known.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a) {
-  constexpr int E2 = D / 64, kEarly = 6;
+template <class S>
+__global__ void __launch_bounds__(32 * S::H) decode_join_few_kernel(const DecodeArgs a) {
+  using T = typename S::T;
+  constexpr int D = S::D, E2 = D / 64, kBatch = 8;
   const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
   dependency_release();
   dependency_wait();
   const int4 j = a.joins[blockIdx.x];
-  if (j.x < 0 || h >= dec_heads_of(a, j)) return;
-  const DecParts<D> p(a, j, h);
+  if (j.x < 0 || h >= dec_heads_of<S>(a, j)) return;
+  const DecParts<S> p(a, j, h);
   auto values = [&](int i, int e) {  // elements 64 e + 2 lane, + 1
     return *reinterpret_cast<const float2*>(p[i] + 64 * e + 2 * lane);
   };
-  float2 early[kEarly][E2];
+  float2 v[kBatch][E2];
+  auto fetch = [&](int i0) {
 #pragma unroll
-  for (int k = 0; k < kEarly; ++k)
+    for (int k = 0; k < kBatch; ++k)
 #pragma unroll
-    for (int e = 0; e < E2; ++e) early[k][e] = k < p.n ? values(k, e) : make_float2(0.f, 0.f);
+      for (int e = 0; e < E2; ++e) v[k][e] = i0 + k < p.n ? values(i0 + k, e) : make_float2(0.f, 0.f);
+  };
+  fetch(0);
   // each lane a part's maximum and sum, 32 at a time
   float mm = -INFINITY, ll = 0.f, acc[2 * E2] = {};
   for (int i0 = 0; i0 < p.n; i0 += 32) {
@@ -973,26 +1016,17 @@ __global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a
     ll = ll * scale + warp_sum(l * f);
 #pragma unroll
     for (int e = 0; e < 2 * E2; ++e) acc[e] *= scale;
-    auto add = [&](int k, const float2 (&v)[E2]) {
-      const float w = __shfl_sync(0xffffffffu, f, k);
+    for (int k0 = 0; k0 < min(32, p.n - i0); k0 += kBatch) {
+      if (i0 + k0 > 0) fetch(i0 + k0);
 #pragma unroll
-      for (int e = 0; e < E2; ++e) {
-        acc[2 * e] = fmaf(v[e].x, w, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(v[e].y, w, acc[2 * e + 1]);
+      for (int k = 0; k < kBatch; ++k) {
+        const float w = __shfl_sync(0xffffffffu, f, k0 + k);  // 0 behind the last part
+#pragma unroll
+        for (int e = 0; e < E2; ++e) {
+          acc[2 * e] = fmaf(v[k][e].x, w, acc[2 * e]);
+          acc[2 * e + 1] = fmaf(v[k][e].y, w, acc[2 * e + 1]);
+        }
       }
-    };
-    int k = 0;
-    if (i0 == 0) {
-#pragma unroll
-      for (int x = 0; x < kEarly; ++x)
-        if (x < p.n) add(x, early[x]);
-      k = kEarly;
-    }
-    for (; k < min(32, p.n - i0); ++k) {
-      float2 v[E2];
-#pragma unroll
-      for (int e = 0; e < E2; ++e) v[e] = values(i0 + k, e);
-      add(k, v);
     }
   }
 #pragma unroll
@@ -1006,16 +1040,18 @@ __global__ void __launch_bounds__(256) decode_join_few_kernel(const DecodeArgs a
 // every G-th part (65793 keys of one sequence come in 74 parts: 28 us as a chain of
 // dependent loads, 3 us so).
 constexpr int kJoinThreads = 512;
-template <typename T, int D>
+template <class S>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_many_kernel(const DecodeArgs a) {
+  using T = typename S::T;
+  constexpr int D = S::D;
   constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
   __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
   dependency_release();
   dependency_wait();
   const int4 j = a.joins[blockIdx.x];
-  if (j.x < 0 || h >= dec_heads_of(a, j)) return;
-  const DecParts<D> p(a, j, h);
+  if (j.x < 0 || h >= dec_heads_of<S>(a, j)) return;
+  const DecParts<S> p(a, j, h);
   const int e = tid % D, g = tid / D;
   float early[kEarly];
 #pragma unroll
@@ -1063,7 +1099,16 @@ namespace {
 struct DecLayout {
   size_t status, joins, part, total;
 };
-DecLayout dec_layout(int d) {
+// Query heads of a run: those of a KV head in one run where its kernel can hold them
+// (bf16 16, fp32 8), in the smallest form that does: 144 bf16 sequences of 2987 keys, 12
+// heads of 64 on one KV head, 24 us in one run of 16 and 34 in two of 8; fp32, 4 sequences up
+// to 88849 keys with 4 heads on each of 2 KV heads, 92 us in a run of 4 and 108 in one of 8.
+int dec_heads(int group, int dtype) {
+  if (dtype == ADASPARK_BF16) return group <= 8 ? 8 : 16;
+  return group <= 2 ? 2 : group <= 4 ? 4 : 8;
+}
+
+DecLayout dec_layout(int d, int heads) {
   DecLayout L{};
   size_t o = align_up(sizeof(WsHeader));
   L.status = o;
@@ -1071,7 +1116,7 @@ DecLayout dec_layout(int d) {
   L.joins = o;
   o = align_up(o + kDecMaxBlocks * sizeof(int4));
   L.part = o;
-  o = align_up(o + (size_t)kDecMaxBlocks * 2 * kDecHeads * (d + 2) * sizeof(float));
+  o = align_up(o + (size_t)kDecMaxBlocks * 2 * heads * (d + 2) * sizeof(float));
   L.total = o;
   return L;
 }
@@ -1084,7 +1129,12 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   // no more blocks than tiles the tables can hold
   const int64_t runs = (int64_t)a.n_seqs * a.hkv * a.hgroups;
   const int64_t tiles = runs * dec_run_tiles(a.max_len, S::kTile);
-  int64_t grid = S::kBlocks * (int64_t)sms;
+  // Blocks per SM: two, and three where the kernel allows it and blocks walk several runs
+  // each: 256 bf16 sequences up to 300 keys, 28 heads on 4, 23 us at three and 25 at two; 61
+  // sequences up to 9001 keys, 16 heads on 2, 52 and 49 us. fp32 runs of 2 or 4 heads always
+  // three.
+  const int per_sm = sizeof(typename S::T) == 2 && runs <= sms ? 2 : S::kBlocks;
+  int64_t grid = per_sm * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;
   if (grid > tiles) grid = tiles;
   a.in_page = a.cs.page_size % S::kKeys == 0;
@@ -1104,19 +1154,23 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
                                     C, a, C));
   }
   a.by_run = runs <= grid;
-  int rc = allow_smem(decode_kernel<M>, S::kSmem);
+  // Two to an SM ask for so much shared memory that a third does not fit: else the blocks of a
+  // call that comes up while the last one's join runs pile up on some SMs (61 sequences, back
+  // to back: 60 us instead of 56).
+  const int smem = per_sm == 2 ? std::max(S::kSmem, 80 << 10) : S::kSmem;
+  int rc = allow_smem(decode_kernel<M>, smem);
   if (rc == ADASPARK_OK)
     rc = cuda_status(launch_after("decode_attn", decode_kernel<M>, dim3((unsigned)grid),
-                                  dim3(kDecWarps * 32), S::kSmem, s, 1, a));
+                                  dim3(kDecWarps * 32), smem, s, 1, a));
   if (rc != ADASPARK_OK) return rc;
   // Parts per run, about: from some 16 on their loads go side by side in a block.
   const unsigned entries = (unsigned)(a.by_run ? runs : grid);
   if (grid / runs >= 16)
-    return cuda_status(launch_after("decode_join", decode_join_many_kernel<typename S::T, S::D>,
-                                    dim3(entries, a.group < kDecHeads ? a.group : kDecHeads),
+    return cuda_status(launch_after("decode_join", decode_join_many_kernel<S>,
+                                    dim3(entries, a.group < S::H ? a.group : S::H),
                                     dim3(kJoinThreads), 0, s, 1, a));
-  return cuda_status(launch_after("decode_join", decode_join_few_kernel<typename S::T, S::D>,
-                                  dim3(entries), dim3(32 * kDecHeads), 0, s, 1, a));
+  return cuda_status(launch_after("decode_join", decode_join_few_kernel<S>, dim3(entries),
+                                  dim3(32 * S::H), 0, s, 1, a));
 }
 
 }  // namespace
@@ -1128,7 +1182,7 @@ extern "C" {
 
 size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dtype) {
   if (n_seqs < 1 || n_seqs > kMaxSeqs || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
-  return dec_layout(d).total;
+  return dec_layout(d, dec_heads(hq / hkv, dtype)).total;
 }
 
 int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* k_cache,
@@ -1143,7 +1197,7 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
   if (!cache_ok(k_cache, v_cache, cs, hkv, d, dtype)) return ADASPARK_EINVAL;
   if ((int64_t)max_pages * page_size > INT32_MAX - 1024) return ADASPARK_EINVAL;
-  const int hgroups = (hq / hkv + kDecHeads - 1) / kDecHeads;
+  const int heads = dec_heads(hq / hkv, dtype), hgroups = (hq / hkv + heads - 1) / heads;
   const int tile = 4096 / (d * (int)elem_size(dtype)) * kDecWarps;
   if ((int64_t)n_seqs * hkv * hgroups * dec_run_tiles((int64_t)max_pages * page_size, tile) >
       INT32_MAX)
@@ -1157,7 +1211,7 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   int sms = 0;
   const int rc = current_device(&sms);
   if (rc != ADASPARK_OK) return rc;
-  const DecLayout L = dec_layout(d);
+  const DecLayout L = dec_layout(d, heads);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeArgs a{};
   a.hdr = reinterpret_cast<WsHeader*>(ws);
@@ -1173,9 +1227,21 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   a.joins = reinterpret_cast<int4*>(ws + L.joins);
   a.part = reinterpret_cast<float*>(ws + L.part);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == ADASPARK_BF16)
-    return d == 128 ? launch_decode<DecBf16<128>>(a, sms, s) : launch_decode<DecBf16<64>>(a, sms, s);
-  return d == 128 ? launch_decode<DecFp32<128>>(a, sms, s) : launch_decode<DecFp32<64>>(a, sms, s);
+  if (dtype == ADASPARK_BF16) {
+    if (heads == 8)
+      return d == 128 ? launch_decode<DecBf16<128, 1>>(a, sms, s)
+                      : launch_decode<DecBf16<64, 1>>(a, sms, s);
+    return d == 128 ? launch_decode<DecBf16<128, 2>>(a, sms, s)
+                    : launch_decode<DecBf16<64, 2>>(a, sms, s);
+  }
+  if (heads == 2)
+    return d == 128 ? launch_decode<DecFp32<128, 2>>(a, sms, s)
+                    : launch_decode<DecFp32<64, 2>>(a, sms, s);
+  if (heads == 4)
+    return d == 128 ? launch_decode<DecFp32<128, 4>>(a, sms, s)
+                    : launch_decode<DecFp32<64, 4>>(a, sms, s);
+  return d == 128 ? launch_decode<DecFp32<128, 8>>(a, sms, s)
+                  : launch_decode<DecFp32<64, 8>>(a, sms, s);
 }
 
 }  // extern "C"

@@ -102,7 +102,8 @@ LENS = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 300, 0, 513]
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("hq,hkv,d", [(28, 4, 128), (16, 2, 128), (4, 1, 64), (6, 3, 64), (3, 3, 128),
-                                      (16, 1, 128), (9, 1, 64), (24, 2, 128)])
+                                      (16, 1, 128), (9, 1, 64), (24, 2, 128),
+                                      (20, 1, 128), (40, 1, 64)])
 @pytest.mark.parametrize("spare_cols", [0, 3000])
 def test_lengths_and_heads(hq, hkv, d, dtype, spare_cols):
     """Tables as long as the longest sequence (a cluster of blocks per run), and
@@ -137,10 +138,11 @@ def test_pages_and_layouts(page, dtype, d, heads_outer):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
-@pytest.mark.parametrize("n", [5000, 20011])
-def test_one_long_sequence(n, dtype):
+@pytest.mark.parametrize("n,hq,hkv", [(5000, 7, 1), (20011, 7, 1), (9000, 12, 1), (4000, 2, 2),
+                                      (3000, 32, 2)])
+def test_one_long_sequence(n, hq, hkv, dtype):
     """Cut over all blocks and joined."""
-    case = _make([n], 7, 1, 128, dtype, 64, seed=n)
+    case = _make([n], hq, hkv, 128, dtype, 64, seed=n)
     _check(*case, *_run(*case))
 
 
