@@ -395,7 +395,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks) decode_kernel(c
   __shared__ DecShared sh;
   __shared__ typename M::Shared msh;
   const int warp = threadIdx.x >> 5;
-  dependency_release();
   dependency_wait();
   uint32_t bits = 0;
   const DecLine L = dec_begin<S>(a, sh, &bits);
@@ -482,7 +481,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
   __shared__ DecShared sh;
   __shared__ typename M::Shared msh;
   __shared__ float part[S::H][D + 2];   // this block's outputs, maxima, sums
-  dependency_release();
   dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = blockIdx.x % C, runs = a.hkv * a.hgroups;
@@ -989,7 +987,6 @@ __global__ void __launch_bounds__(32 * S::H) decode_join_few_kernel(const Decode
   using T = typename S::T;
   constexpr int D = S::D, E2 = D / 64, kBatch = 8;
   const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
-  dependency_release();
   dependency_wait();
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0 || h >= dec_heads_of<S>(a, j)) return;
@@ -1047,7 +1044,6 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_many_kernel(const De
   constexpr int G = kJoinThreads / D, W = kJoinThreads / 32, kEarly = 16;
   __shared__ float f[kDecMaxBlocks], red[2][W], acc_g[G][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
-  dependency_release();
   dependency_wait();
   const int4 j = a.joins[blockIdx.x];
   if (j.x < 0 || h >= dec_heads_of<S>(a, j)) return;

@@ -28,6 +28,7 @@ struct PlanArgs {
   int32_t *starts, *slots, *positions;
   int32_t *take0, *give0;        // workspace: pages taken / given by earlier sequences
   int32_t n_seqs, max_pages, page_size, n_pages, n_rows;
+  int32_t chunk;                 // rows a warp takes at a time
   uint32_t div_mul, div_shift;   // n / page_size = n * div_mul >> div_shift for 0 <= n < 2^31
 };
 
@@ -234,9 +235,8 @@ __device__ __forceinline__ void plan_row(const PlanArgs& a, int r, int pos, int 
 __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
                                            const PlanTotals& t, int warp, int warps) {
   const int lane = threadIdx.x & 31, rows = t.ok ? t.rows : 0;
-  const int chunk = a.n_rows <= warps * 32 ? 32 : 128;
-  for (int r0 = warp * chunk; r0 < a.n_rows; r0 += warps * chunk) {
-    const int r1 = min(r0 + chunk, a.n_rows), r2 = min(r1, rows);
+  for (int r0 = warp * a.chunk; r0 < a.n_rows; r0 += warps * a.chunk) {
+    const int r1 = min(r0 + a.chunk, a.n_rows), r2 = min(r1, rows);
     for (int r = max(r0, rows) + lane; r < r1; r += 32) {
       a.slots[r] = -1;
       a.positions[r] = 0;
@@ -298,7 +298,6 @@ __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ PlanShared sh;
-  dependency_release();
   dependency_wait();
   const PlanTotals t = plan_sums<true>(a, &sh);
   __syncthreads();   // the status is there for plan_write's flags
@@ -307,19 +306,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs a) {
-  dependency_release();
   dependency_wait();
   const PlanTotals t = plan_sums<false>(a, nullptr);
   if (threadIdx.x == 0) *plan_totals(a.hdr) = t;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_write_kernel(const PlanArgs a) {
+constexpr int kPlanWriteThreads = 256;
+__global__ void __launch_bounds__(kPlanWriteThreads) plan_write_kernel(const PlanArgs a) {
   __shared__ PlanShared sh;
-  dependency_release();
   dependency_wait();
   PlanSums p{a.old_lens, a.new_lens, a.take0, a.give0, a.starts};
   if (a.n_seqs <= kPlanSeqs) {
-    for (int i = threadIdx.x; i < a.n_seqs; i += kPlanThreads) {
+    for (int i = threadIdx.x; i < a.n_seqs; i += kPlanWriteThreads) {
       sh.old_lens[i] = a.old_lens[i];
       sh.new_lens[i] = a.new_lens[i];
       sh.take0[i] = a.take0[i];
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_write_kernel(const PlanArgs
     __syncthreads();
     p = {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts};
   }
-  constexpr int W = kPlanThreads / 32;
+  constexpr int W = kPlanWriteThreads / 32;
   plan_write(a, p, *plan_totals(a.hdr), blockIdx.x * W + (threadIdx.x >> 5), gridDim.x * W);
 }
 
@@ -387,16 +385,20 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   if (n_rows <= kPlanOneBlock && n_seqs <= kPlanSeqs) {
     // no more warps than sequences and rows give work
     const int threads = std::min(kPlanThreads, (std::max(n_seqs, n_rows) + 127) / 128 * 128);
+    a.chunk = (n_rows + threads - 1) / threads * 32;
     return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(threads), 0, s, 1, a));
   }
   cudaError_t e =
       launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
   if (e == cudaSuccess) {
-    const int64_t want = ((int64_t)n_rows + 4095) / 4096;  // 128 rows a warp
-    const int64_t most = (int64_t)sms * 2;
-    const unsigned grid = (unsigned)(want < most ? want : most);
-    e = launch_after("kv_plan_write", plan_write_kernel, dim3(grid), dim3(kPlanThreads), 0,
-                     s, 1, a);
+    // two blocks per SM; finding a warp's first row costs as much as writing some 400, so the
+    // rows of a warp grow with the plan (825 thousand rows: 8 us at 128 rows a warp)
+    constexpr int W = kPlanWriteThreads / 32;
+    const int64_t most = (int64_t)sms * 2, share = (n_rows + most * W * 32 - 1) / (most * W * 32);
+    a.chunk = (int)std::min<int64_t>(share, 16) * 32;
+    const int64_t want = ((int64_t)n_rows + a.chunk * W - 1) / (a.chunk * W);
+    e = launch_after("kv_plan_write", plan_write_kernel, dim3((unsigned)std::min(want, most * 4)),
+                     dim3(kPlanWriteThreads), 0, s, 1, a);
   }
   return cuda_status(e);
 }

@@ -272,7 +272,6 @@ __global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_walk_kernel(const Ro
   constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
-  dependency_release();
   dependency_wait();
   const int lane = threadIdx.x & 31, grp = lane / M::kLanes;
   const int stride = gridDim.x * 4;
@@ -354,7 +353,6 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
   constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
-  dependency_release();
   dependency_wait();
   const int lane = threadIdx.x & 31, grp = lane / M::kLanes;
   const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
@@ -413,7 +411,6 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   constexpr int V = kBwdRun;
   using M = RopeMap<D, V>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
-  dependency_release();
   dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / M::kLanes;
   int e0, e1;
@@ -559,7 +556,6 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
 __global__ void __launch_bounds__(1024)
     rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
   __shared__ float sum[128][9];
-  dependency_release();
   dependency_wait();
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int col = blockIdx.x * 8 + x;
