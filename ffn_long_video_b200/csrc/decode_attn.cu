@@ -55,18 +55,6 @@ constexpr int kDecMaxBlocks = 148 * 3;
 constexpr int kDecCluster = 8;   // blocks that join through shared memory, at most
 constexpr float kLn2 = 0.69314718055994530942f;
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool there) {
-  const int bytes = there ? 16 : 0;  // nothing is read for 0; the 16 bytes become zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Sizes of a warp's work: a tile is kKeys keys of each of the block's warps, a
 // stage a warp's share of it, a ring the stages it has in flight. bf16 rows are
 // padded so that the 8 rows of a matrix load fall on different banks.

@@ -50,11 +50,13 @@ constexpr int kRopeRun = 8;
 template <typename T>
 constexpr int kRopeBlocks = sizeof(T) == 2 ? 7 : 5;
 // Backward: runs of 4 elements (half the values per lane beside 32 sums for the
-// weights), 5 blocks on an SM. 18560 tokens of 16 + 2 normalised heads: 73 us at 5
-// (floor 66), 77 at 4 and at 6; runs of 8 at 3 blocks 73; 154 us before the next
-// step's rows were loaded ahead.
+// weights), three steps ahead, 6 blocks on an SM. 18560 tokens of 16 + 2 normalised
+// heads, weights' gradient included, calls one after another: 78.6 us (floor 66),
+// 81.8 at 5 blocks, 85 at 7, 82.6 at 8 blocks and two steps; one step ahead in
+// registers 82.5; 161 with nothing ahead.
 constexpr int kBwdRun = 4;
-constexpr int kBwdBlocksPerSm = 5;
+constexpr int kBwdAhead = 3;
+constexpr int kBwdBlocksPerSm = 6;
 
 // A head's lanes, each with two runs of V elements.
 template <int D, int V>
@@ -400,17 +402,93 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
     row.store(static_cast<T*>(part == 1 ? a.kc : a.vc) + slot + h * a.cs.hs + e0, gap);
 }
 
+// Rows of the backward pass on their way: lane-private slots in shared memory, a
+// ring of kBwdAhead + 1 steps filled by cp.async (registers would hold one step
+// ahead). The walk: queries, then keys, then the warp's next token.
+template <typename T, typename T2, int D, int V, bool NORM>
+struct BwdRing {
+  using M = RopeMap<D, V>;
+  static constexpr int kDy = V * (int)sizeof(T2), kX = V * (int)sizeof(T);  // bytes of a run
+  static constexpr int kStep = 32 * 2 * (kDy + (NORM ? kX : 0));
+  static constexpr int kSlots = kBwdAhead + 1;
+  static constexpr int kWarp = kSlots * kStep;
+
+  const RopeArgs& a;
+  const T2 *dq0, *dk0, *dy;   // of this lane's first run
+  const T *q0, *k0, *x;
+  HeadRows dqs, dks;
+  uint8_t* slots;             // this lane's part of the warp's ring
+  int gap, grp, stride, q_steps, k_steps;
+  int t, h, left, slot;
+  bool keys;
+
+  __device__ __forceinline__ void start(int token) {
+    t = token;
+    keys = false;
+    h = grp;
+    left = q_steps;
+    slot = 0;
+    dy = dq0 + t * dqs.ts;
+    x = q0 + t * a.qs.ts;
+  }
+  // Copies the walk's step into the next slot and moves on; one commit group.
+  __device__ __forceinline__ void fetch() {
+    if (t < a.n) {
+      if (h < (keys ? a.hkv : a.hq)) {
+        uint8_t* s = slots + slot * kStep;
+        cp_async<kDy>(s, dy);
+        cp_async<kDy>(s + 32 * kDy, dy + gap);
+        if (NORM && (keys ? a.wk : a.wq)) {
+          // rows start on 16 bytes, a lane's runs on 8 or 16 of them
+          uint8_t* sx = slot_x(slot);
+          cp_async<kX>(sx, x);
+          cp_async<kX>(sx + 32 * kX, x + gap);
+        }
+      }
+      h += M::kHeads;
+      if (--left > 0) {
+        dy += M::kHeads * (keys ? dks.hs : dqs.hs);
+        x += M::kHeads * (keys ? a.ks.hs : a.qs.hs);
+      } else {
+        h = grp;
+        keys = !keys;
+        left = keys ? k_steps : q_steps;
+        if (!keys) t += stride;
+        dy = keys ? dk0 + t * dks.ts : dq0 + t * dqs.ts;
+        x = keys ? k0 + t * a.ks.ts : q0 + t * a.qs.ts;
+      }
+    }
+    cp_async_commit();
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+  }
+  __device__ __forceinline__ uint8_t* slot_x(int i) const {
+    const int lane = threadIdx.x & 31;
+    return slots - lane * kDy + i * kStep + 64 * kDy + lane * kX;
+  }
+  __device__ __forceinline__ void row(int i, RopeRow<T2, V>& dy_row, RopeRow<T, V>& x_row) const {
+    const uint8_t* s = slots + i * kStep;
+    dy_row.u.load(reinterpret_cast<const T2*>(s));
+    dy_row.v.load(reinterpret_cast<const T2*>(s + 32 * kDy));
+    if (NORM) {
+      const uint8_t* sx = slot_x(i);
+      x_row.u.load(reinterpret_cast<const T*>(sx));
+      x_row.v.load(reinterpret_cast<const T*>(sx + 32 * kX));
+    }
+  }
+};
+
 // Backward: warps walk tokens with a fixed stride, so the partial sums of the
-// weights' gradients have a fixed order; each block writes one row of them. The
-// next step's rows are on their way while a step is computed. dy in T2, x in T,
-// dx in fp32.
+// weights' gradients have a fixed order; each block writes one row of them.
+// dy in T2, x in T, dx in fp32.
 template <typename T, typename T2, int D, bool IL, bool NORM>
 __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
     rope_bwd_kernel(const RopeArgs a, const void* dq, const void* dk, HeadRows dqs, HeadRows dks,
                     float* gq, float* gk, float* part) {
   constexpr int V = kBwdRun;
   using M = RopeMap<D, V>;
+  using Ring = BwdRing<T, T2, D, V, NORM>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
+  __shared__ __align__(16) uint8_t rings[4 * Ring::kWarp];
   dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / M::kLanes;
   int e0, e1;
@@ -418,31 +496,42 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   const int gap = e1 - e0, stride = gridDim.x * 4;
   const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
   const int k_steps = (a.hkv + M::kHeads - 1) / M::kHeads;
-  const T2* const dq0 = static_cast<const T2*>(dq) + grp * dqs.hs + e0;
-  const T2* const dk0 = static_cast<const T2*>(dk) + grp * dks.hs + e0;
-  const T* const q0 = static_cast<const T*>(a.q) + grp * a.qs.hs + e0;
-  const T* const k0 = static_cast<const T*>(a.k) + grp * a.ks.hs + e0;
   const bool has_q = NORM && a.wq, has_k = NORM && a.wk;
   F2 dwq[V] = {}, dwk[V] = {};
-  RopeRow<T2, V> ndy{};
-  RopeRow<T, V> nx{};
-  auto first = [&](int t) {
-    if (t < a.n && grp < a.hq) {
-      ndy.load(dq0 + t * dqs.ts, gap);
-      if (has_q) nx.load(q0 + t * a.qs.ts, gap);
-    }
-  };
   int t = blockIdx.x * 4 + warp;
-  first(t);
+  Ring ring{a,
+            static_cast<const T2*>(dq) + grp * dqs.hs + e0,
+            static_cast<const T2*>(dk) + grp * dks.hs + e0,
+            nullptr,
+            static_cast<const T*>(a.q) + grp * a.qs.hs + e0,
+            static_cast<const T*>(a.k) + grp * a.ks.hs + e0,
+            nullptr,
+            dqs,
+            dks,
+            rings + warp * Ring::kWarp + lane * Ring::kDy,
+            gap,
+            grp,
+            stride,
+            q_steps,
+            k_steps};
+  ring.start(t);
+#pragma unroll
+  for (int i = 0; i < kBwdAhead; ++i) ring.fetch();
   const RopePairs<D, IL, V> pairs(a, lane);
   int pos[M::kAngles] = {};
   if (t < a.n) pairs.positions(a, t, pos);
   if constexpr (NORM) rope_weights<T, D>(a, weights);
   RopeTurn<D, IL, V> rotation;
+  int slot = 0;
 
-  // dx of a row from dy (in u, v) and x; its weights' gradient onto dw.
-  auto head = [&](const RopeRow<T2, V>& dy, const RopeRow<T, V>& xr, const float* w, bool has_w,
-                  F2 (&dw)[V], float* o, bool mine) {
+  // dx of the next row from dy and x; its weights' gradient onto dw.
+  auto head = [&](const float* w, bool has_w, F2 (&dw)[V], float* o, bool mine) {
+    ring.fetch();  // into the slot that the step before has used up
+    cp_async_wait<kBwdAhead>();
+    RopeRow<T2, V> dy;
+    RopeRow<T, V> xr;
+    ring.row(slot, dy, xr);
+    slot = slot + 1 == Ring::kSlots ? 0 : slot + 1;
     F2 u[V / 2], v[V / 2];
     dy.u.get(u);
     dy.v.get(v);
@@ -489,46 +578,18 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   for (; t < a.n; t += stride) {
     rotation.template set<true>(a, pairs, pos, lane);
     if (t + stride < a.n) pairs.positions(a, t + stride, pos);
-    const T2* p = dq0 + t * dqs.ts;
-    const T* x = q0 + t * a.qs.ts;
     float* o = gq + ((int64_t)t * a.hq + grp) * D + e0;
     for (int h = grp, st = 0; st < q_steps; ++st, h += M::kHeads) {
-      const RopeRow<T2, V> dy = ndy;
-      const RopeRow<T, V> xr = nx;
-      p += M::kHeads * dqs.hs;
-      x += M::kHeads * a.qs.hs;
-      if (st + 1 < q_steps) {
-        if (h + M::kHeads < a.hq) {
-          ndy.load(p, gap);
-          if (has_q) nx.load(x, gap);
-        }
-      } else if (grp < a.hkv) {
-        ndy.load(dk0 + t * dks.ts, gap);
-        if (has_k) nx.load(k0 + t * a.ks.ts, gap);
-      }
-      head(dy, xr, weights[0], has_q, dwq, o, h < a.hq);
+      head(weights[0], has_q, dwq, o, h < a.hq);
       o += M::kHeads * D;
     }
-    p = dk0 + t * dks.ts;
-    x = k0 + t * a.ks.ts;
     o = gk + ((int64_t)t * a.hkv + grp) * D + e0;
     for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
-      const RopeRow<T2, V> dy = ndy;
-      const RopeRow<T, V> xr = nx;
-      p += M::kHeads * dks.hs;
-      x += M::kHeads * a.ks.hs;
-      if (st + 1 < k_steps) {
-        if (h + M::kHeads < a.hkv) {
-          ndy.load(p, gap);
-          if (has_k) nx.load(x, gap);
-        }
-      } else {
-        first(t + stride);
-      }
-      head(dy, xr, weights[NORM ? 1 : 0], has_k, dwk, o, h < a.hkv);
+      head(weights[NORM ? 1 : 0], has_k, dwk, o, h < a.hkv);
       o += M::kHeads * D;
     }
   }
+  cp_async_wait<0>();
   if constexpr (NORM) {
     __shared__ float sum[4 * M::kHeads][2][D];
     float(*mine)[D] = sum[warp * M::kHeads + grp];
