@@ -20,12 +20,6 @@
 
 namespace adaspark {
 
-#ifndef DSF
-#define DSF 2
-#define DBF 3
-#define DSB 3
-#define DBB 2
-#endif
 struct DecodeArgs {
   WsHeader* hdr;
   const void* q;
@@ -277,8 +271,9 @@ __device__ __forceinline__ uint32_t dec_copy(const DecodeArgs& a, uint8_t* st, c
     uint8_t* kd = st + r0 * S::kRow + piece * 16;
     uint8_t* vd = kd + S::kKeys * S::kRow;
     if (a.in_page && there == S::kAll) {
-      // a page holds all rows: they lie ts apart, one offset serves (a third less to issue
-      // per row than an exchange for each)
+      // a page holds all rows: they lie ts apart and one offset serves (fp32, 24 sequences of
+      // 20000 to 30001 keys, one call after another: 443 us, 459 with an exchange per row;
+      // bf16 the same either way)
       const int64_t o0 = __shfl_sync(0xffffffffu, off, 0);
       const int64_t byte = (o0 + r0 * a.cs.ts) * es + piece * 16, step = rows * a.cs.ts * es;
       const uint8_t* ks = static_cast<const uint8_t*>(a.kc) + byte;

@@ -42,8 +42,9 @@ __device__ __forceinline__ PlanTotals* plan_totals(WsHeader* h) {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 1024;      // sequences whose sums are kept in shared memory
-// Up to here one block writes a plan's rows, 4 each thread: 64 sequences that gain 161
-// tokens 5.7 us against 7.8 for two kernels, 4096 rows 8.2 against 8.1.
+// Up to here one block writes a plan's rows, 4 each thread. Plans one after another: 64
+// sequences that gain 161 tokens 3.2 us against 5.1 with two kernels; 4000 tokens of 250
+// sequences 6.6 against 6.7, of one sequence 5.8 against 5.5.
 constexpr int kPlanOneBlock = 4096;
 
 // Per-sequence values that the writes search, in shared memory or (more than
@@ -243,7 +244,8 @@ __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
     }
     if (r0 >= r2) continue;
     int s = plan_find_warp(p.starts, a.n_seqs, r0);
-    if (plan_find_warp(p.starts, a.n_seqs, r2 - 1) - s < 8) {
+    const int span = plan_find_warp(p.starts, a.n_seqs, r2 - 1) + 1 - s;
+    if (span <= 8) {
       // few sequences: the warp looks up 32 pages of one at a time
       for (int ra = r0; ra < r2; ++s) {
         const int st = p.starts[s], rb = s + 1 < a.n_seqs ? min(r2, p.starts[s + 1]) : r2;
@@ -275,8 +277,9 @@ __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
       }
     } else {
       // many sequences: a lane looks up its own row
+      const int s0 = s;
       for (int r = r0 + lane; r < r2; r += 32) {
-        while (s + 1 < a.n_seqs && p.starts[s + 1] <= r) ++s;
+        s = s0 + plan_find(p.starts + s0, span, r);
         const int o = p.old_lens[s], pos = o + r - p.starts[s], col = plan_div(a, pos);
         const int held = plan_pages(a, o), i = p.take0[s] + col - held;
         int page;
@@ -391,8 +394,8 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   cudaError_t e =
       launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
   if (e == cudaSuccess) {
-    // two blocks per SM; finding a warp's first row costs as much as writing some 400, so the
-    // rows of a warp grow with the plan (825 thousand rows: 8 us at 128 rows a warp)
+    // two blocks per SM until each warp has 512 rows (it has to find its first one), then more
+    // blocks
     constexpr int W = kPlanWriteThreads / 32;
     const int64_t most = (int64_t)sms * 2, share = (n_rows + most * W * 32 - 1) / (most * W * 32);
     a.chunk = (int)std::min<int64_t>(share, 16) * 32;
