@@ -10,9 +10,11 @@
 // from old to new, free list included. A plan that cannot be carried out
 // changes nothing.
 //
-// Latency-bound: one block sums the sequences' takes, gifts and new tokens and, for
-// a step's few rows, writes slots, table and list entries as well; for many rows
-// (prompts) a second kernel writes them over the whole GPU.
+// Latency-bound: a block sums the sequences' takes, gifts and new tokens and writes
+// slots, table and list entries. A step's few rows take one block; many rows
+// (prompts) the whole GPU, where every block sums for itself, nobody reads what
+// another block writes, and the free count, which all of them read, follows in a
+// second kernel. Sequences that are too many for that are summed by a kernel ahead.
 #include <algorithm>
 
 #include "serve.h"
@@ -26,9 +28,11 @@ struct PlanArgs {
   int64_t table_stride;
   int32_t *free_pages, *n_free;
   int32_t *starts, *slots, *positions;
+  int32_t* status;               // workspace: status bits of each block
   int32_t *take0, *give0;        // workspace: pages taken / given by earlier sequences
   int32_t n_seqs, max_pages, page_size, n_pages, n_rows;
   int32_t chunk;                 // rows a warp takes at a time
+  int32_t blocks;                // blocks that write status words (0: the header holds all)
   uint32_t div_mul, div_shift;   // n / page_size = n * div_mul >> div_shift for 0 <= n < 2^31
 };
 
@@ -42,9 +46,12 @@ __device__ __forceinline__ PlanTotals* plan_totals(WsHeader* h) {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSeqs = 1024;      // sequences whose sums are kept in shared memory
-// Up to here one block writes a plan's rows, 4 each thread. Plans one after another: 64
-// sequences that gain 161 tokens 3.2 us against 5.1 with two kernels; 4000 tokens of 250
-// sequences 6.6 against 6.7, of one sequence 5.8 against 5.5.
+// Up to here one block writes a plan's rows, 4 each thread. Plans one after another, one
+// block and all: 64 sequences that gain 161 tokens 3.0 and 4.5 us, 250 that gain 4000 5.6 and
+// 6.3, 8000 6.6 and 5.6. 300 sequences, a third of them gone and a third new with 825
+// thousand tokens: 7.8 us (7 MB of slots, positions and page numbers: 1 us at 6.46 TB/s; the
+// rest is one launch, three dependent reads and the second launch), 10.2 with the sums in a
+// kernel of their own.
 constexpr int kPlanOneBlock = 4096;
 
 // Per-sequence values that the writes search, in shared memory or (more than
@@ -80,14 +87,15 @@ __device__ __forceinline__ void warp_scan3(I (&v)[3]) {
   }
 }
 
-// Sums over the sequences (one block of whole warps), the plan's check, its totals;
-// n_free and the status are written here. KEEP: the sums stay in shared memory
-// (n_seqs <= kPlanSeqs), else they go to the workspace.
+// Sums over the sequences (a block of whole warps), the plan's check, its totals;
+// block 0 writes starts and status and, with COUNT, n_free. KEEP: the sums stay in
+// shared memory (n_seqs <= kPlanSeqs), else they go to the workspace.
 constexpr int kPlanTooMuch = 1 << 21;  // 1024 values below it sum up in 31 bits
-template <bool KEEP>
+template <bool KEEP, bool COUNT>
 __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* sh) {
   __shared__ int warp_sum[2][kPlanThreads / 32][3];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool first = blockIdx.x == 0;
   const long long F = *a.n_free;
   const long long most = (long long)a.max_pages * a.page_size;
   long long carry[3] = {0, 0, 0};
@@ -156,7 +164,7 @@ __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* s
       (KEEP ? sh->take0 : a.take0)[i] = (int32_t)(carry[0] + before[0]);
       (KEEP ? sh->give0 : a.give0)[i] = (int32_t)(carry[1] + before[1]);
       if (KEEP) sh->starts[i] = (int32_t)(carry[2] + before[2]);
-      a.starts[i] = (int32_t)(carry[2] + before[2]);
+      if (first) a.starts[i] = (int32_t)(carry[2] + before[2]);
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) carry[k] += total[k];
@@ -168,15 +176,15 @@ __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* s
   const bool sound = !any_bad && carry[2] <= a.n_rows && F >= 0 && F <= a.n_pages &&
                      carry[1] <= a.n_pages && left <= a.n_pages;
   const bool ok = sound && left >= 0;
-  if (!ok)
+  if (!ok && first)
     for (int i = threadIdx.x; i < a.n_seqs; i += blockDim.x) a.starts[i] = 0;
   const PlanTotals t{ok, (int32_t)carry[2], (int32_t)carry[0], (int32_t)carry[1], (int32_t)F};
-  if (threadIdx.x == 0) {
+  if (first && threadIdx.x == 0) {
     a.starts[a.n_seqs] = ok ? t.rows : 0;
-    if (ok) *a.n_free = (int32_t)left;
+    if (COUNT && ok) *a.n_free = (int32_t)left;
     a.hdr->status = ok ? 0u : sound ? ADASPARK_DEV_PAGES : ADASPARK_DEV_BAD_LAYOUT;
     a.hdr->detail = ok ? 0u : 0x8100u;
-    a.hdr->n_block_status = 0;
+    a.hdr->n_block_status = a.blocks;
   }
   return t;
 }
@@ -220,22 +228,25 @@ __device__ __forceinline__ int plan_taken(const PlanArgs& a, const PlanSums& p,
   return i < t.give ? plan_given(a, p, i, s) : a.free_pages[t.n_free - 1 - (i - t.give)];
 }
 
-__device__ __forceinline__ void plan_row(const PlanArgs& a, int r, int pos, int page, int in_page) {
+__device__ __forceinline__ void plan_row(const PlanArgs& a, int r, int pos, int page, int in_page,
+                                         bool* bad) {
   int slot = -1;
   if (page >= 0 && page < a.n_pages)
     slot = page * a.page_size + in_page;
   else
-    set_status(a.hdr, ADASPARK_DEV_BAD_LAYOUT, 0x8200u);
+    *bad = true;
   a.slots[r] = slot;
   a.positions[r] = pos;
 }
 
 // Slots, positions, table and list entries, by `warps` warps of which this is
 // `warp`. A page that is taken is written to its table by whoever has its first
-// token, which is always a new one.
-__device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
+// token, which is always a new one. Returns whether this thread met a page number
+// that the pool does not have.
+__device__ __forceinline__ bool plan_write(const PlanArgs& a, const PlanSums& p,
                                            const PlanTotals& t, int warp, int warps) {
   const int lane = threadIdx.x & 31, rows = t.ok ? t.rows : 0;
+  bool bad = false;
   for (int r0 = warp * a.chunk; r0 < a.n_rows; r0 += warps * a.chunk) {
     const int r1 = min(r0 + a.chunk, a.n_rows), r2 = min(r1, rows);
     for (int r = max(r0, rows) + lane; r < r1; r += 32) {
@@ -270,7 +281,7 @@ __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
           for (; ra < rc; ra += 32) {
             const int r = min(ra + lane, rc - 1), pos = r + shift, c = plan_div(a, pos);
             const int pg = __shfl_sync(0xffffffffu, page, c - c0);
-            if (ra + lane < rc) plan_row(a, r, pos, pg, pos - c * a.page_size);
+            if (ra + lane < rc) plan_row(a, r, pos, pg, pos - c * a.page_size, &bad);
           }
           ra = rc;
         }
@@ -289,50 +300,71 @@ __device__ __forceinline__ void plan_write(const PlanArgs& a, const PlanSums& p,
           page = plan_taken(a, p, t, i, i < t.give ? plan_find(p.give0, a.n_seqs, i) : 0);
           if (col * a.page_size == pos) a.table[s * a.table_stride + col] = page;
         }
-        plan_row(a, r, pos, page, pos - col * a.page_size);
+        plan_row(a, r, pos, page, pos - col * a.page_size, &bad);
       }
     }
   }
-  if (!t.ok) return;
+  if (!t.ok) return bad;
   for (int g = t.take + warp * 32 + lane; g < t.give; g += warps * 32)
     a.free_pages[t.n_free + t.give - 1 - g] =
         plan_given(a, p, g, plan_find(p.give0, a.n_seqs, g));
+  return bad;
+}
+
+__device__ __forceinline__ PlanSums plan_kept(const PlanShared& sh) {
+  return {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts};
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   __shared__ PlanShared sh;
   dependency_wait();
-  const PlanTotals t = plan_sums<true>(a, &sh);
-  __syncthreads();   // the status is there for plan_write's flags
-  plan_write(a, {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts}, t, threadIdx.x >> 5,
-             blockDim.x >> 5);
+  const PlanTotals t = plan_sums<true, true>(a, &sh);
+  __syncthreads();
+  const bool bad = plan_write(a, plan_kept(sh), t, threadIdx.x >> 5, blockDim.x >> 5);
+  if (__syncthreads_or(bad) && threadIdx.x == 0) {
+    a.hdr->status = ADASPARK_DEV_BAD_LAYOUT;
+    a.hdr->detail = 0x8200u;
+  }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs a) {
-  dependency_wait();
-  const PlanTotals t = plan_sums<false>(a, nullptr);
-  if (threadIdx.x == 0) *plan_totals(a.hdr) = t;
+__device__ __forceinline__ void plan_block_status(const PlanArgs& a, bool bad) {
+  const bool any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) a.status[blockIdx.x] = any ? ADASPARK_DEV_BAD_LAYOUT : 0;
 }
 
-constexpr int kPlanWriteThreads = 256;
-__global__ void __launch_bounds__(kPlanWriteThreads) plan_write_kernel(const PlanArgs a) {
+// Many rows, up to kPlanSeqs sequences; n_free is written by plan_count_kernel. One block an
+// SM: 7.8 us for the 825 thousand tokens above, 8.1 with two of half the size, 9.2 with four.
+__global__ void __launch_bounds__(kPlanThreads) plan_wide_kernel(const PlanArgs a) {
   __shared__ PlanShared sh;
   dependency_wait();
-  PlanSums p{a.old_lens, a.new_lens, a.take0, a.give0, a.starts};
-  if (a.n_seqs <= kPlanSeqs) {
-    for (int i = threadIdx.x; i < a.n_seqs; i += kPlanWriteThreads) {
-      sh.old_lens[i] = a.old_lens[i];
-      sh.new_lens[i] = a.new_lens[i];
-      sh.take0[i] = a.take0[i];
-      sh.give0[i] = a.give0[i];
-      sh.starts[i] = a.starts[i];
-    }
-    __syncthreads();
-    p = {sh.old_lens, sh.new_lens, sh.take0, sh.give0, sh.starts};
-  }
-  constexpr int W = kPlanWriteThreads / 32;
-  plan_write(a, p, *plan_totals(a.hdr), blockIdx.x * W + (threadIdx.x >> 5), gridDim.x * W);
+  const PlanTotals t = plan_sums<true, false>(a, &sh);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *plan_totals(a.hdr) = t;
+  __syncthreads();
+  constexpr int W = kPlanThreads / 32;
+  plan_block_status(a, plan_write(a, plan_kept(sh), t, blockIdx.x * W + (threadIdx.x >> 5),
+                                  gridDim.x * W));
 }
+__global__ void plan_count_kernel(const PlanArgs a) {
+  dependency_wait();
+  const PlanTotals t = *plan_totals(a.hdr);
+  if (t.ok) *a.n_free = t.n_free + t.give - t.take;
+}
+
+// More sequences: their sums in the workspace.
+__global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs a) {
+  dependency_wait();
+  const PlanTotals t = plan_sums<false, true>(a, nullptr);
+  if (threadIdx.x == 0) *plan_totals(a.hdr) = t;
+}
+__global__ void __launch_bounds__(kPlanThreads) plan_write_kernel(const PlanArgs a) {
+  dependency_wait();
+  constexpr int W = kPlanThreads / 32;
+  plan_block_status(a, plan_write(a, {a.old_lens, a.new_lens, a.take0, a.give0, a.starts},
+                                  *plan_totals(a.hdr), blockIdx.x * W + (threadIdx.x >> 5),
+                                  gridDim.x * W));
+}
+
+constexpr int kPlanMaxBlocks = 1024;
 
 }  // namespace adaspark
 
@@ -342,7 +374,8 @@ extern "C" {
 
 size_t adaspark_kv_plan_workspace(int n_seqs) {
   if (n_seqs < 1 || n_seqs > kMaxSeqs) return 0;
-  return align_up(sizeof(WsHeader)) + 2 * align_up((size_t)n_seqs * sizeof(int32_t));
+  return align_up(sizeof(WsHeader)) + align_up(kPlanMaxBlocks * sizeof(int32_t)) +
+         2 * align_up((size_t)n_seqs * sizeof(int32_t));
 }
 
 int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seqs, int page_size,
@@ -372,7 +405,8 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PlanArgs a{};
   a.hdr = reinterpret_cast<WsHeader*>(ws);
-  a.take0 = reinterpret_cast<int32_t*>(ws + align_up(sizeof(WsHeader)));
+  a.status = reinterpret_cast<int32_t*>(ws + align_up(sizeof(WsHeader)));
+  a.take0 = a.status + align_up(kPlanMaxBlocks * sizeof(int32_t)) / sizeof(int32_t);
   a.give0 = a.take0 + align_up((size_t)n_seqs * sizeof(int32_t)) / sizeof(int32_t);
   a.old_lens = old_lens; a.new_lens = new_lens;
   a.table = block_table; a.table_stride = table_stride;
@@ -391,17 +425,24 @@ int adaspark_kv_plan(const int32_t* old_lens, const int32_t* new_lens, int n_seq
     a.chunk = (n_rows + threads - 1) / threads * 32;
     return cuda_status(launch_after("kv_plan", plan_kernel, dim3(1), dim3(threads), 0, s, 1, a));
   }
-  cudaError_t e =
-      launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
-  if (e == cudaSuccess) {
-    // two blocks per SM until each warp has 512 rows (it has to find its first one), then more
-    // blocks
-    constexpr int W = kPlanWriteThreads / 32;
-    const int64_t most = (int64_t)sms * 2, share = (n_rows + most * W * 32 - 1) / (most * W * 32);
-    a.chunk = (int)std::min<int64_t>(share, 16) * 32;
-    const int64_t want = ((int64_t)n_rows + a.chunk * W - 1) / (a.chunk * W);
-    e = launch_after("kv_plan_write", plan_write_kernel, dim3((unsigned)std::min(want, most * 4)),
-                     dim3(kPlanWriteThreads), 0, s, 1, a);
+  // blocks that fill the GPU until each warp has 512 rows (it has to find its first one)
+  constexpr int W = kPlanThreads / 32;
+  const bool wide = n_seqs <= kPlanSeqs;
+  const int64_t most = sms;
+  const int64_t share = (n_rows + most * W * 32 - 1) / (most * W * 32);
+  a.chunk = (int)std::min<int64_t>(share, 16) * 32;
+  const int64_t want = ((int64_t)n_rows + a.chunk * W - 1) / (a.chunk * W);
+  a.blocks = (int)std::min({want, wide ? most : 4 * most, (int64_t)kPlanMaxBlocks});
+  const dim3 grid(a.blocks), block(kPlanThreads);
+  cudaError_t e;
+  if (wide) {
+    e = launch_after("kv_plan", plan_wide_kernel, grid, block, 0, s, 1, a);
+    if (e == cudaSuccess)
+      e = launch_after("kv_plan_count", plan_count_kernel, dim3(1), dim3(1), 0, s, 1, a);
+  } else {
+    e = launch_after("kv_plan_sums", plan_sums_kernel, dim3(1), dim3(kPlanThreads), 0, s, 1, a);
+    if (e == cudaSuccess)
+      e = launch_after("kv_plan_write", plan_write_kernel, grid, block, 0, s, 1, a);
   }
   return cuda_status(e);
 }

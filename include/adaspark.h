@@ -619,8 +619,9 @@ size_t adaspark_kv_plan_workspace(int n_seqs);
  * slots -1) and reports ADASPARK_DEV_PAGES (too few free pages) or
  * ADASPARK_DEV_BAD_LAYOUT (a length out of range, more than n_rows new tokens,
  * a free count or a gift the pool cannot hold); a page number outside
- * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. The arrays
- * must not overlap. workspace: 256-byte aligned. ADASPARK_EINVAL for NULL
+ * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. A page
+ * belongs to one sequence or to the list: one that two sequences hold would be
+ * listed twice when both give it back. The arrays must not overlap. workspace: 256-byte aligned. ADASPARK_EINVAL for NULL
  * pointers, sizes < 1, n_seqs > 2^24, n_pages or n_rows > 2^30, a table_stride
  * below max_pages, a short workspace. */
 int adaspark_kv_plan(const int32_t *old_lens, const int32_t *new_lens, int n_seqs, int page_size,
@@ -642,7 +643,7 @@ size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dt
  *       i * table_stride, key j on page block_table[i][j / page_size];
  *   seq_lens [n_seqs]: device int32, 0 .. max_pages * page_size;
  *   scale: finite (1/sqrt(d) in adaspark_cube_attn);
- *   out [n_seqs, hq, d]: device, dense; lse [n_seqs, hq]: device float32 or NULL;
+ *   out [n_seqs, hq, d]: device, dense, may be Q itself; lse [n_seqs, hq]: device float32 or NULL;
  *   workspace: 256-byte aligned.
  * Nothing at or past a sequence's length is read (it may hold NaN). Values that
  * are infinite or NaN among a sequence's keys make its results NaN or infinite.

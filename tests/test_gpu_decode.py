@@ -234,6 +234,19 @@ def test_strides_and_given_outputs():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("lens,spare_cols", [([300, 0, 77], 0), ([300, 0, 4000], 3000),
+                                             ([30] * 200, 0)])
+def test_output_over_the_queries(lens, spare_cols, dtype):
+    """out may be Q itself: the same results as apart."""
+    x = _make(lens, 16, 2, 128, dtype, 16, spare_cols=spare_cols)
+    out, lse = _run(*x)
+    q = x[0].clone()
+    over, lse2 = _run(q, *x[1:], out=q)
+    assert over.data_ptr() == q.data_ptr()
+    assert torch.equal(out, q) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("spare_cols", [0, 3000])
 def test_bad_lengths_and_pages_are_flagged(spare_cols):
     """A length the table cannot hold counts as 0, a page that is not there holds

@@ -164,3 +164,37 @@ def test_captured_steps_share_a_workspace():
             st.same()
             assert [x.tolist() for x in o] == [got[3], got[4], got[5]]
     assert np.array_equal(old, st.lens)
+
+
+@pytest.mark.parametrize("n", [3, 1024, 1500])
+def test_checks_of_plans_over_the_whole_gpu(n):
+    """Many rows: refused plans change nothing, bad pages are flagged from whichever
+    block meets them, the next plan clears the flag, releases fill the list again."""
+    page, cols = 16, 400
+    st = State(n, cols, page, 3 * cols + n)
+    long = np.ones(n, int)
+    long[:3] = (6000, 0, 5999)
+    *_, (code, det) = st.step(long, int(long.sum()) - 1)
+    assert code == fb.EDEVICE and det & 0xff == fb.DEV_BAD_LAYOUT
+    *_, (code, det) = st.step(np.full(n, 6400), n * 6400 if n == 3 else 10000)
+    if n > 3:
+        assert code == fb.EDEVICE and det & 0xff == fb.DEV_BAD_LAYOUT
+        over = np.ones(n, int)
+        over[:4] = 6400                             # enough rows, too few pages
+        *_, (code, det) = st.step(over, 30000)
+        assert code == fb.EDEVICE and det & 0xff == fb.DEV_PAGES
+    st.step(long, 16000)
+    st.d_table[2, 374] = st.d_table[2, 374] + 10 ** 6     # the last page of sequence 2
+    more = st.lens.copy()
+    more[2] = 5999 + 1                              # its next token lies on that page
+    slots, _, starts, ws = fb.kv_plan(_t(st.lens), _t(more), st.d_table, st.d_free, st.d_n, page,
+                                      9000)
+    assert fb.read_device_status(ws)[1] & 0xff == fb.DEV_BAD_LAYOUT
+    assert starts[-1].item() == 1 and torch.all(slots == -1)
+    st.d_table[2, 374] = st.d_table[2, 374] - 10 ** 6
+    *_, ws = fb.kv_plan(_t(st.lens), _t(more), st.d_table, st.d_free, st.d_n, page, 9000,
+                        workspace=ws)
+    assert fb.read_device_status(ws)[0] == fb.OK
+    *_, ws = fb.kv_plan(_t(more), _t(0 * more), st.d_table, st.d_free, st.d_n, page, 5000)
+    assert fb.read_device_status(ws)[0] == fb.OK
+    assert sorted(st.d_free.tolist()) == list(range(3 * cols + n)) and st.d_n.item() == 3 * cols + n
