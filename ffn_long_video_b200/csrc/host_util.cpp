@@ -96,7 +96,7 @@ int device_is_sm100() {
   return (major == 10 && minor == 0) ? 1 : 0;
 }
 
-int allow_smem(const void* kernel, int bytes, bool no_l1) {
+int allow_smem(const void* kernel, int bytes) {
   struct Known {
     const void* kernel;
     int device, bytes;
@@ -110,9 +110,6 @@ int allow_smem(const void* kernel, int bytes, bool no_l1) {
     if (k.kernel == kernel && k.device == dev && k.bytes >= bytes) return ADASPARK_OK;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
       cudaSuccess)
-    return ADASPARK_ECUDA;
-  if (no_l1 && cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                    cudaSharedmemCarveoutMaxShared) != cudaSuccess)
     return ADASPARK_ECUDA;
   try {
     known.push_back({kernel, dev, bytes});

@@ -31,12 +31,11 @@ inline cudaError_t launch(const char* name, void (*kernel)(KArgs...), dim3 grid,
 }
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device; asked
-// of the runtime once per kernel and device. `no_l1`: its SMs keep as little of their
-// memory as L1 cache as they can (the runtime's own split may hold fewer blocks).
-int allow_smem(const void* kernel, int bytes, bool no_l1 = false);
+// of the runtime once per kernel and device.
+int allow_smem(const void* kernel, int bytes);
 template <typename... KArgs>
-inline int allow_smem(void (*kernel)(KArgs...), int bytes, bool no_l1 = false) {
-  return allow_smem(reinterpret_cast<const void*>(kernel), bytes, no_l1);
+inline int allow_smem(void (*kernel)(KArgs...), int bytes) {
+  return allow_smem(reinterpret_cast<const void*>(kernel), bytes);
 }
 
 // launch() of a kernel whose blocks may come up while the stream's previous

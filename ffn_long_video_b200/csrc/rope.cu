@@ -16,6 +16,7 @@
 // exchange, and the norm's sum takes log2(d/16) shuffles. Angles are reduced to a
 // turn in 64 bits (positions of 2^20 and more keep full fp32 accuracy), sines and
 // cosines, norms and rotations are in 32 bits and outputs rounded once.
+#include <algorithm>
 #include <cmath>
 
 #include "serve.h"
@@ -43,20 +44,24 @@ constexpr double kInvTwoPi = 0.15915494309189533577;
 // Forward: runs of 8 elements, 7 blocks on an SM for bf16 (72 registers). 65792
 // tokens of 28 + 4 heads of 128: 162 us at 7, 169 at 6, 181 at 5, 171 at 9
 // (spills); 18559 normalised tokens of 16 + 2 heads: 28, 31, 33 and 29 us (the
-// floors at 6.46 TB/s: 167 and 26.5 us). Before that, with one loop over queries
-// and keys that selects its pointers a step: 163 and 34 us; with blocks that end
-// after a token: 190 and 42 us.
+// floors at 6.46 TB/s: 167 and 26.5 us); with blocks that end after a token 190 and
+// 42 us.
 constexpr int kRopeRun = 8;
 template <typename T>
 constexpr int kRopeBlocks = sizeof(T) == 2 ? 7 : 5;
-// Backward: runs of 4 elements (half the values per lane beside 32 sums for the
-// weights), three steps ahead, 6 blocks on an SM. 18560 tokens of 16 + 2 normalised
-// heads, weights' gradient included, calls one after another: 78.6 us (floor 66),
-// 81.8 at 5 blocks, 85 at 7, 82.6 at 8 blocks and two steps; one step ahead in
-// registers 82.5; 161 with nothing ahead.
+// Backward: runs of 4 elements (half the values per lane beside 32 sums for the weights).
+// With norms 3 blocks on an SM, rows three steps ahead: fewer warps keep the memory's order
+// better. 18560 tokens of 16 + 2 normalised heads of 128, weights' gradient included, calls one
+// after another: 71.8 us (floor 66); 78.6 at 6 blocks, 87.9 at 2, 74.3 two steps ahead, 71.7
+// five; 161 with nothing ahead. Without norms two steps ahead (three: as at 6 blocks) and 3
+// blocks for many tokens, 6 for up to two tokens a warp: 30001 tokens of 16 + 2 heads 86.4 and
+// 93.0 us, 9999 of 28 + 4 53.0 and 56.7, 2999 11.9 and 11.1.
 constexpr int kBwdRun = 4;
-constexpr int kBwdAhead = 3;
-constexpr int kBwdBlocksPerSm = 6;
+template <bool NORM>
+constexpr int kBwdAhead = NORM ? 3 : 2;
+template <bool NORM>
+constexpr int kBwdBlocksPerSm = NORM ? 3 : 6;   // residents
+constexpr int kBwdLongBlocks = 3;
 
 // A head's lanes, each with two runs of V elements.
 template <int D, int V>
@@ -267,87 +272,150 @@ __device__ __forceinline__ int64_t rope_slot(const RopeArgs& a, int t) {
   return page * a.cs.ps + (slot - page * a.cs.page_size) * a.cs.ts;
 }
 
+constexpr int kRopeAhead = 2;
+// Rows on their way, in the order of the walk: queries, keys, (with a cache) values,
+// then the warp's next token. RING: lane-private slots in shared memory, filled by
+// cp.async kRopeAhead steps ahead; else registers, one step ahead.
+template <typename T, int D, int V, bool CACHE, bool RING>
+struct RopeRing {
+  using M = RopeMap<D, V>;
+  static constexpr int kPieces = V * (int)sizeof(T) / 16;  // 16-byte pieces of a run
+  static constexpr int kStep = 32 * 16 * 2 * kPieces, kSlots = kRopeAhead + 1;
+  static constexpr int kWarp = RING ? kSlots * kStep : 0;
+  static constexpr int kAhead = RING ? kRopeAhead : 1;
+
+  const RopeArgs& a;
+  const T *q0, *k0, *v0, *p;  // of this lane's first run
+  uint8_t* slots;             // this lane's part of the warp's ring
+  int gap, grp, stride, q_steps, k_steps;
+  int t, h, left, in, out, part;
+  RopeRow<T, V> next;
+
+  __device__ __forceinline__ void start(int token) {
+    t = token;
+    h = grp;
+    left = q_steps;
+    in = out = part = 0;
+    p = q0 + t * a.qs.ts;
+  }
+  // Copies the walk's step into the next slot and moves on; one commit group.
+  __device__ __forceinline__ void fetch() {
+    if (t < a.n) {
+      if (h < (part ? a.hkv : a.hq)) {
+        if (RING) {
+          uint8_t* s = slots + in * kStep;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            cp_async<16>(s + 512 * i, p + i * (16 / (int)sizeof(T)));
+            cp_async<16>(s + 512 * (kPieces + i), p + gap + i * (16 / (int)sizeof(T)));
+          }
+        } else {
+          next.load(p, gap);
+        }
+      }
+      h += M::kHeads;
+      if (--left > 0) {
+        p += M::kHeads * (part == 0 ? a.qs.hs : part == 1 ? a.ks.hs : a.vs.hs);
+      } else {
+        h = grp;
+        part = part == (CACHE ? 2 : 1) ? 0 : part + 1;
+        left = part ? k_steps : q_steps;
+        if (part == 0) t += stride;
+        p = part == 0 ? q0 + t * a.qs.ts : part == 1 ? k0 + t * a.ks.ts : v0 + t * a.vs.ts;
+      }
+    }
+    if (RING) {
+      cp_async_commit();
+      in = in + 1 == kSlots ? 0 : in + 1;
+    }
+  }
+  // The next row of the walk; a step is copied into the slot that the one before has used up.
+  __device__ __forceinline__ RopeRow<T, V> take() {
+    RopeRow<T, V> r = next;
+    fetch();
+    if (!RING) return r;
+    cp_async_wait<kRopeAhead>();
+    const uint8_t* s = slots + out * kStep;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(s + 512 * i);
+      const uint4 y = *reinterpret_cast<const uint4*>(s + 512 * (kPieces + i));
+      r.u.w[4 * i] = x.x; r.u.w[4 * i + 1] = x.y; r.u.w[4 * i + 2] = x.z; r.u.w[4 * i + 3] = x.w;
+      r.v.w[4 * i] = y.x; r.v.w[4 * i + 1] = y.y; r.v.w[4 * i + 2] = y.z; r.v.w[4 * i + 3] = y.w;
+    }
+    out = out + 1 == kSlots ? 0 : out + 1;
+    return r;
+  }
+};
+
 // Many tokens: warps walk tokens; queries, then keys, then (with a cache) values,
-// which are copied. The next step's row, of the next token too, is on its way
-// while a step is computed.
-template <typename T, int D, bool IL, bool CACHE, bool NORM, bool FULL>
+// which are copied.
+template <typename T, int D, bool IL, bool CACHE, bool NORM, bool FULL, bool RING>
 __global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_walk_kernel(const RopeArgs a) {
   constexpr int V = kRopeRun;
   using M = RopeMap<D, V>;
+  using Ring = RopeRing<T, D, V, CACHE, RING>;
   __shared__ __align__(16) float weights[2][NORM ? D : 1];
+  extern __shared__ __align__(16) uint8_t rings[];
   dependency_wait();
-  const int lane = threadIdx.x & 31, grp = lane / M::kLanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / M::kLanes;
   const int stride = gridDim.x * 4;
   int e0, e1;
   rope_runs<V>(lane % M::kLanes, a.rot, &e0, &e1);
   const int gap = e1 - e0;
   const int q_steps = (a.hq + M::kHeads - 1) / M::kHeads;
   const int k_steps = (a.hkv + M::kHeads - 1) / M::kHeads;
-  const T* const q0 = static_cast<const T*>(a.q) + grp * a.qs.hs + e0;
-  const T* const k0 = static_cast<const T*>(a.k) + grp * a.ks.hs + e0;
-  int t = blockIdx.x * 4 + (threadIdx.x >> 5);
-  RopeRow<T, V> next{};
-  if (t < a.n && grp < a.hq) next.load(q0 + t * a.qs.ts, gap);
+  int t = blockIdx.x * 4 + warp;
+  Ring ring{a,
+            static_cast<const T*>(a.q) + grp * a.qs.hs + e0,
+            static_cast<const T*>(a.k) + grp * a.ks.hs + e0,
+            CACHE ? static_cast<const T*>(a.v) + grp * a.vs.hs + e0 : nullptr,
+            nullptr,
+            rings + warp * Ring::kWarp + lane * 16,
+            gap,
+            grp,
+            stride,
+            q_steps,
+            k_steps};
+  ring.start(t);
+#pragma unroll
+  for (int i = 0; i < Ring::kAhead; ++i) ring.fetch();
   const RopePairs<D, IL, V> pairs(a, lane);
   int pos[M::kAngles] = {};
   if (t < a.n) pairs.positions(a, t, pos);
   if constexpr (NORM) rope_weights<T, D>(a, weights);
   RopeTurn<D, IL, V, FULL> rotation;
   for (; t < a.n; t += stride) {
-    const int t2 = t + stride;
     const int64_t slot = rope_slot<T, CACHE>(a, t);
     rotation.template set<false>(a, pairs, pos, lane);
-    if (t2 < a.n) pairs.positions(a, t2, pos);
-    const T* p = q0 + t * a.qs.ts;
+    if (t + stride < a.n) pairs.positions(a, t + stride, pos);
     T* o = static_cast<T*>(a.qo) + t * a.qos.ts + grp * a.qos.hs + e0;
     for (int h = grp, st = 0; st < q_steps; ++st, h += M::kHeads) {
-      RopeRow<T, V> row = next;
-      p += M::kHeads * a.qs.hs;
-      if (st + 1 < q_steps) {
-        if (h + M::kHeads < a.hq) next.load(p, gap);
-      } else if (grp < a.hkv) {
-        next.load(k0 + t * a.ks.ts, gap);
-      }
+      RopeRow<T, V> row = ring.take();
       rope_head<T, D, IL, NORM>(row, rotation, weights[0], a.wq != nullptr, e0, gap, a.eps);
       if (h < a.hq) row.store(o, gap);
       o += M::kHeads * a.qos.hs;
     }
-    p = k0 + t * a.ks.ts;
     const int64_t ostep = M::kHeads * (CACHE ? a.cs.hs : a.kos.hs);
     o = CACHE ? static_cast<T*>(a.kc) + (slot + grp * a.cs.hs + e0)
               : static_cast<T*>(a.ko) + t * a.kos.ts + grp * a.kos.hs + e0;
-    const T* const v0 = CACHE ? static_cast<const T*>(a.v) + t * a.vs.ts + grp * a.vs.hs + e0 : nullptr;
     for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
-      RopeRow<T, V> row = next;
-      p += M::kHeads * a.ks.hs;
-      if (st + 1 < k_steps) {
-        if (h + M::kHeads < a.hkv) next.load(p, gap);
-      } else if (CACHE) {
-        if (grp < a.hkv) next.load(v0, gap);
-      } else if (t2 < a.n && grp < a.hq) {
-        next.load(q0 + t2 * a.qs.ts, gap);
-      }
+      RopeRow<T, V> row = ring.take();
       rope_head<T, D, IL, NORM>(row, rotation, weights[NORM ? 1 : 0], a.wk != nullptr, e0, gap,
-                                   a.eps);
+                                a.eps);
       if (h < a.hkv && (!CACHE || slot >= 0)) row.store(o, gap);
       o += ostep;
     }
     if (CACHE) {
-      p = v0;
       o = static_cast<T*>(a.vc) + (slot + grp * a.cs.hs + e0);
       for (int h = grp, st = 0; st < k_steps; ++st, h += M::kHeads) {
-        const RopeRow<T, V> row = next;
-        p += M::kHeads * a.vs.hs;
-        if (st + 1 < k_steps) {
-          if (h + M::kHeads < a.hkv) next.load(p, gap);
-        } else if (t2 < a.n && grp < a.hq) {
-          next.load(q0 + t2 * a.qs.ts, gap);
-        }
+        const RopeRow<T, V> row = ring.take();
         if (h < a.hkv && slot >= 0) row.store(o, gap);
         o += ostep;
       }
     }
   }
+  if (RING) cp_async_wait<0>();
 }
 
 // Few tokens, and keys and values alone (hq = 0): a warp per step of a token's heads.
@@ -404,14 +472,14 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
 }
 
 // Rows of the backward pass on their way: lane-private slots in shared memory, a
-// ring of kBwdAhead + 1 steps filled by cp.async (registers would hold one step
+// ring of kAhead + 1 steps filled by cp.async (registers would hold one step
 // ahead). The walk: queries, then keys, then the warp's next token.
 template <typename T, typename T2, int D, int V, bool NORM>
 struct BwdRing {
   using M = RopeMap<D, V>;
   static constexpr int kDy = V * (int)sizeof(T2), kX = V * (int)sizeof(T);  // bytes of a run
   static constexpr int kStep = 32 * 2 * (kDy + (NORM ? kX : 0));
-  static constexpr int kSlots = kBwdAhead + 1;
+  static constexpr int kAhead = kBwdAhead<NORM>, kSlots = kAhead + 1;
   static constexpr int kWarp = kSlots * kStep;
 
   const RopeArgs& a;
@@ -482,7 +550,7 @@ struct BwdRing {
 // weights' gradients have a fixed order; each block writes one row of them.
 // dy in T2, x in T, dx in fp32.
 template <typename T, typename T2, int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(128, kBwdBlocksPerSm)
+__global__ void __launch_bounds__(128, kBwdBlocksPerSm<NORM>)
     rope_bwd_kernel(const RopeArgs a, const void* dq, const void* dk, HeadRows dqs, HeadRows dks,
                     float* gq, float* gk, float* part) {
   constexpr int V = kBwdRun;
@@ -517,7 +585,7 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
             k_steps};
   ring.start(t);
 #pragma unroll
-  for (int i = 0; i < kBwdAhead; ++i) ring.fetch();
+  for (int i = 0; i < Ring::kAhead; ++i) ring.fetch();
   const RopePairs<D, IL, V> pairs(a, lane);
   int pos[M::kAngles] = {};
   if (t < a.n) pairs.positions(a, t, pos);
@@ -528,7 +596,7 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm)
   // dx of the next row from dy and x; its weights' gradient onto dw.
   auto head = [&](const float* w, bool has_w, F2 (&dw)[V], float* o, bool mine) {
     ring.fetch();  // into the slot that the step before has used up
-    cp_async_wait<kBwdAhead>();
+    cp_async_wait<Ring::kAhead>();
     RopeRow<T2, V> dy;
     RopeRow<T, V> xr;
     ring.row(slot, dy, xr);
@@ -660,7 +728,7 @@ bool qk_rope_args_ok(const double* freq, int rot, int d, const int32_t* position
 
 namespace {
 
-constexpr int kBwdMaxBlocks = 148 * kBwdBlocksPerSm;
+constexpr int kBwdMaxParts = 148 * kBwdBlocksPerSm<true>;  // blocks with sums for the weights
 
 void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions, int n_axes,
               const int32_t* sections, float magnitude, int n) {
@@ -672,6 +740,24 @@ void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions
   a->sec01 = n_axes == 3 ? sections[0] + sections[1] : rot / 2;
   a->magnitude = magnitude;
   a->n = n;
+}
+
+// bf16 rows up to this size are read through the ring, two steps ahead. Calls one after
+// another, ring and registers: 2999 tokens of 16 + 2 heads of 128 5.8 and 7.0 us, 18559 (85
+// MB) normalised 29.9 and 33.4; 9999 of 28 + 4 28.3 and 30.0, 14999 (123 MB) 43.3 and 41.9,
+// 65792 182 and 167: there the reads that run ahead disturb the memory's order, which warps in
+// step keep. Three steps ahead cost 0.3 us of 30, one 0.5. fp32, 4999 tokens: 25 and 18 us.
+constexpr int64_t kRopeRingBytes = 100 << 20;
+
+template <typename T, int D, bool CACHE, bool NORM, bool RING>
+cudaError_t launch_walk(const RopeArgs& a, bool il, const char* name, dim3 grid, cudaStream_t s) {
+  auto* kernel = a.rot == D ? (il ? rope_walk_kernel<T, D, true, CACHE, NORM, true, RING>
+                                  : rope_walk_kernel<T, D, false, CACHE, NORM, true, RING>)
+                            : (il ? rope_walk_kernel<T, D, true, CACHE, NORM, false, RING>
+                                  : rope_walk_kernel<T, D, false, CACHE, NORM, false, RING>);
+  constexpr int smem = 4 * RopeRing<T, D, kRopeRun, CACHE, RING>::kWarp;
+  if (smem && allow_smem(kernel, smem) != ADASPARK_OK) return cudaErrorUnknown;
+  return launch_after(name, kernel, grid, dim3(128), smem, s, 1, a);
 }
 
 template <typename T, int D, bool CACHE, bool NORM>
@@ -689,11 +775,10 @@ cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
   if (walk) {
     const int64_t want = (n + 3) / 4, most = (int64_t)sms * kRopeBlocks<T>;
     const dim3 grid((unsigned)(want < most ? want : most));
-    auto* kernel = a.rot == D ? (il ? rope_walk_kernel<T, D, true, CACHE, NORM, true>
-                                    : rope_walk_kernel<T, D, false, CACHE, NORM, true>)
-                              : (il ? rope_walk_kernel<T, D, true, CACHE, NORM, false>
-                                    : rope_walk_kernel<T, D, false, CACHE, NORM, false>);
-    return launch_after(name, kernel, grid, block, 0, s, 1, a);
+    const int64_t bytes = n * (a.hq + a.hkv * (CACHE ? 2 : 1)) * D * (int64_t)sizeof(T);
+    if constexpr (sizeof(T) == 2)
+      if (bytes <= kRopeRingBytes) return launch_walk<T, D, CACHE, NORM, true>(a, il, name, grid, s);
+    return launch_walk<T, D, CACHE, NORM, false>(a, il, name, grid, s);
   }
   if (n * steps > INT32_MAX - 3) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((n * steps + 3) / 4));
@@ -727,8 +812,6 @@ struct BwdCall {
 template <typename T, typename T2, int D, bool NORM>
 cudaError_t launch_bwd(const BwdCall& b, bool il, cudaStream_t s) {
   auto* kernel = il ? rope_bwd_kernel<T, T2, D, true, NORM> : rope_bwd_kernel<T, T2, D, false, NORM>;
-  // 17 KB a block (bf16): left to itself the runtime makes room for five, 82.6 us instead of 78.6
-  if (allow_smem(kernel, 0, true) != ADASPARK_OK) return cudaErrorUnknown;
   return launch_after("qk_rope_backward", kernel, dim3(b.blocks), dim3(128), 0, s, 1, b.a, b.dq,
                       b.dk, b.dqs, b.dks, b.gq, b.gk, b.part);
 }
@@ -869,7 +952,7 @@ int adaspark_kv_append(const void* K, int64_t k_ts, int64_t k_hs, const void* V,
 
 size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d, int dtype) {
   if (n_tokens < 0 || n_tokens > (1 << 30) || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
-  return align_up((size_t)kBwdMaxBlocks * 2 * d * sizeof(float));
+  return align_up((size_t)kBwdMaxParts * 2 * d * sizeof(float));
 }
 
 int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, const void* dK_out,
@@ -919,9 +1002,12 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
   b.a.wq = w_q; b.a.wk = w_k; b.a.eps = eps; b.a.hq = hq; b.a.hkv = hkv;
   b.dq = dQ_out; b.dk = dK_out; b.dqs = {dq_ts, dq_hs}; b.dks = {dk_ts, dk_hs};
   b.gq = dQ; b.gk = dK; b.part = static_cast<float*>(workspace);
-  int blocks = sms * kBwdBlocksPerSm;
-  if (blocks > kBwdMaxBlocks) blocks = kBwdMaxBlocks;
-  if (blocks > (n_tokens + 3) / 4) blocks = (n_tokens + 3) / 4;
+  int blocks = sms * kBwdBlocksPerSm<false>;
+  if (norm)
+    blocks = std::min(sms * kBwdBlocksPerSm<true>, kBwdMaxParts);
+  else if (n_tokens > blocks * 4 * 2)
+    blocks = sms * kBwdLongBlocks;
+  blocks = std::min(blocks, (n_tokens + 3) / 4);
   b.blocks = blocks;
   const bool il = interleaved != 0;
   using bf16 = __nv_bfloat16;
