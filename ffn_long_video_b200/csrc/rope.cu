@@ -419,6 +419,8 @@ __global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_walk_kernel(const Ro
 }
 
 // Few tokens, and keys and values alone (hq = 0): a warp per step of a token's heads.
+// Latency-bound: one token of 28 + 4 normalised heads, one call after another, 2.4 us,
+// 200 tokens of 16 + 2 heads 2.1 us.
 template <typename T, int D, bool IL, bool CACHE, bool NORM>
 __global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
   constexpr int V = kRopeRun;
@@ -685,7 +687,7 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm<NORM>)
 }
 
 // Sums the blocks' rows, 8 columns per block: column c of rows y, y + 128, ..., then
-// over y in halves.
+// over y in halves. Latency-bound: 2.6 us for 444 rows of 256.
 __global__ void __launch_bounds__(1024)
     rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
   __shared__ float sum[128][9];
