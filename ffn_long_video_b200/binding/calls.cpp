@@ -1,7 +1,8 @@
 // The generation calls from Python: argument checks, allocation and the C call in
 // one step. These calls run once per layer and generated token, where the host
 // time of a call counts: through ctypes a decode call took 20 us on the host, 14
-// of them for checks, allocation and argument conversion; this way it is 8.
+// of them for checks, allocation and argument conversion; this way an append takes
+// 4.7 us on the host (3.1 with its output given), a decode call 5.6.
 //
 // Positional arguments only (the package's functions name and document them);
 // None stands for an output or a workspace to be allocated. Checks raise

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(128, kRopeBlocks<T>) rope_walk_kernel(const Ro
   if (RING) cp_async_wait<0>();
 }
 
-// Few tokens, and keys and values alone (hq = 0): a warp per step of a token's heads.
+// Few tokens: a warp per step of a token's heads.
 // Latency-bound: one token of 28 + 4 normalised heads, one call after another, 2.4 us,
 // 200 tokens of 16 + 2 heads 2.1 us.
 template <typename T, int D, bool IL, bool CACHE, bool NORM>
@@ -471,6 +471,42 @@ __global__ void __launch_bounds__(128) rope_step_kernel(const RopeArgs a) {
     row.store(static_cast<T*>(a.ko) + t * a.kos.ts + h * a.kos.hs + e0, gap);
   else if (slot >= 0)
     row.store(static_cast<T*>(part == 1 ? a.kc : a.vc) + slot + h * a.cs.hs + e0, gap);
+}
+
+// Keys and values as they are into the cache, 16 bytes at a time, kCopyAhead of them in
+// flight per thread. HBM-bound: 65792 tokens of 4 heads of 128, bf16, one call after another
+// 44.1 us (floor 41.7), 18559 of 2 heads 8.9 (5.9), 64 tokens 2.6; with two in flight 46.1, 8.8
+// and 1.9, with eight 47.3, 9.3 and 4.0; a warp per token's heads 48.7 and 14.1.
+constexpr int kCopyThreads = 128, kCopyAhead = 4;
+template <typename T, int D>
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const RopeArgs a) {
+  constexpr int kPer = 16 / (int)sizeof(T), kPieces = D / kPer;  // pieces of a head
+  dependency_wait();
+  const int row = a.hkv * kPieces, both = 2 * row;
+  // the block's first piece: of token t0, r0 pieces into its keys and values
+  const int64_t base = (int64_t)blockIdx.x * (kCopyThreads * kCopyAhead);
+  const int t0 = (int)(base / both), r0 = (int)(base - (int64_t)t0 * both);
+  uint4 v[kCopyAhead];
+  T* to[kCopyAhead];
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i) {
+    const int r = r0 + i * kCopyThreads + (int)threadIdx.x, dt = r / both, t = t0 + dt;
+    to[i] = nullptr;
+    if (t >= a.n) continue;
+    const int64_t slot = rope_slot<T, true>(a, t);
+    if (slot < 0) continue;
+    int p = r - dt * both;
+    const bool value = p >= row;
+    if (value) p -= row;
+    const int h = p / kPieces, e = p % kPieces * kPer;
+    const HeadRows s = value ? a.vs : a.ks;
+    v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(value ? a.v : a.k) + t * s.ts +
+                                           h * s.hs + e);
+    to[i] = static_cast<T*>(value ? a.vc : a.kc) + slot + h * a.cs.hs + e;
+  }
+#pragma unroll
+  for (int i = 0; i < kCopyAhead; ++i)
+    if (to[i]) *reinterpret_cast<uint4*>(to[i]) = v[i];
 }
 
 // Rows of the backward pass on their way: lane-private slots in shared memory, a
@@ -770,8 +806,8 @@ cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
   // A warp per step while that gives the longest-running warp less to do than walking whole
   // tokens; a token's angles count as a step and a half.
   const int64_t warps = (int64_t)sms * kRopeBlocks<T> * 4;
-  const bool walk = a.hq > 0 && ((n + warps - 1) / warps) * (steps + 1.5) <
-                                    ((n * steps + warps - 1) / warps) * 2.5;
+  const bool walk =
+      ((n + warps - 1) / warps) * (steps + 1.5) < ((n * steps + warps - 1) / warps) * 2.5;
   const char* name = CACHE ? "qk_rope_append" : "qk_rope";
   const dim3 block(128);
   if (walk) {
@@ -801,6 +837,15 @@ cudaError_t dispatch_rope(const RopeArgs& a, int dtype, int d, bool il, int sms,
                     : launch_rope<__nv_bfloat16, 64, CACHE>(a, il, sms, s);
   return d == 128 ? launch_rope<float, 128, CACHE>(a, il, sms, s)
                   : launch_rope<float, 64, CACHE>(a, il, sms, s);
+}
+
+template <typename T>
+cudaError_t launch_copy(const RopeArgs& a, int d, cudaStream_t s) {
+  const int64_t pieces = (int64_t)a.n * 2 * a.hkv * (d * (int)sizeof(T) / 16);
+  const int64_t blocks = (pieces - 1) / (kCopyThreads * kCopyAhead) + 1;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_after("kv_append", d == 128 ? kv_copy_kernel<T, 128> : kv_copy_kernel<T, 64>,
+                      dim3((unsigned)blocks), dim3(kCopyThreads), 0, s, 1, a);
 }
 
 struct BwdCall {
@@ -944,12 +989,12 @@ int adaspark_kv_append(const void* K, int64_t k_ts, int64_t k_hs, const void* V,
   int sms = 0;
   const int rc = current_device(&sms);
   if (rc != ADASPARK_OK) return rc;
-  // the append kernel with no query heads and nothing rotated
   RopeArgs a{};
   a.n = n_tokens; a.k = K; a.v = V; a.ks = {k_ts, k_hs}; a.vs = {v_ts, v_hs};
   a.hkv = hkv; a.slots = slots; a.kc = k_cache; a.vc = v_cache; a.cs = cs;
-  return cuda_status(dispatch_rope<true>(a, dtype, d, false, sms,
-                                         static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(dtype == ADASPARK_BF16 ? launch_copy<__nv_bfloat16>(a, d, s)
+                                            : launch_copy<float>(a, d, s));
 }
 
 size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d, int dtype) {

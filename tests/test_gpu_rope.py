@@ -239,6 +239,43 @@ def test_append_far_slots():
     assert int((kc[-3:] != 0).any(dim=-1).sum()) == 40 * hkv
 
 
+@pytest.mark.parametrize("n,h,d,dtype", [(1, 1, 64, BF16), (1000, 3, 64, FP32), (513, 7, 128, BF16),
+                                         (3001, 2, 128, FP32), (77, 40, 128, BF16)])
+def test_append_of_shared_and_strided_rows(n, h, d, dtype):
+    """Keys shared by all heads (head stride 0), values a part of wider rows."""
+    g = torch.Generator().manual_seed(n)
+    K = _rand(g, n, 1, d, dtype=dtype).expand(n, h, d)
+    V = _rand(g, n, h + 2, d + 16, dtype=dtype)[:, 1:h + 1, 16:]
+    pages = -(-n // 5) + 1
+    kc, vc = (torch.zeros(pages, 5, h, d, dtype=dtype, device="cuda") for _ in range(2))
+    slots = torch.randperm(pages * 5, generator=g)[:n].to(torch.int32).cuda()
+    fb.kv_append(K, V, slots, kc, vc)
+    s = slots.long()
+    want_k, want_v = torch.zeros_like(kc), torch.zeros_like(vc)
+    want_k[s // 5, s % 5], want_v[s // 5, s % 5] = K, V
+    assert torch.equal(kc, want_k) and torch.equal(vc, want_v)
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_many_tokens_are_the_same_as_a_few(dtype, norm):
+    """Tokens do not depend on each other: a long call, in whatever form its size
+    selects, gives the bits of calls on its parts; so does the gradient's dx."""
+    n, hq, hkv, d = 20003, 28, 4, 128
+    g = torch.Generator().manual_seed(2)
+    Q, K = _rand(g, n, hq, d, dtype=dtype), _rand(g, n, hkv, d, dtype=dtype)
+    w = dict(w_q=_rand(g, d, dtype=dtype), w_k=_rand(g, d, dtype=dtype)) if norm else {}
+    pos = torch.arange(n, dtype=torch.int32, device="cuda") * 7
+    freq = torch.from_numpy(fb.rope_frequencies(d)[0]).cuda()
+    q, k = fb.qk_rope(Q, K, pos, freq, **w)
+    dQ, dK, *_ = fb.qk_rope_backward(q, k, pos, freq, Q, K, **w)
+    for a, b in ((0, 1), (1, 200), (200, 7000), (7000, n)):
+        q2, k2 = fb.qk_rope(Q[a:b], K[a:b], pos[a:b], freq, **w)
+        assert torch.equal(q[a:b], q2) and torch.equal(k[a:b], k2)
+        dq2, dk2, *_ = fb.qk_rope_backward(q2, k2, pos[a:b], freq, Q[a:b], K[a:b], **w)
+        assert torch.equal(dQ[a:b], dq2) and torch.equal(dK[a:b], dk2)
+
+
 # -------------------------------------------------------------------------- gradient
 def _grad_bound(dy, x, w, ang, c, dy_rot):
     """Bounds of dx and of one dw term.  g carries 34 u of its pair's length G,
