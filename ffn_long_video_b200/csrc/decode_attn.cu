@@ -6,7 +6,7 @@
 //
 // Bound by the cache's bytes: each key and value is read once for all the query
 // heads of its KV head. The work is cut into tiles of keys, and all tiles of all
-// (sequence, KV head, group of 8 query heads) runs are laid on one line that the
+// (sequence, KV head, group of query heads) runs are laid on one line that the
 // blocks share evenly, whatever the lengths: block b of B takes tiles
 // [b T / B, (b + 1) T / B). A block keeps the running maximum, sum and output of
 // the run it is in; a run that lies in one block is finished there, a cut one
@@ -61,10 +61,10 @@ struct DecShape {
   static constexpr int kRow = D * (int)sizeof(T) + (sizeof(T) == 2 ? 16 : 0);
   static constexpr int kStage = 2 * kKeys * kRow;            // K rows, V rows
   static constexpr int kStages = 2;
-  // Blocks per SM (registers and shared memory allow no more): fp32 with 8 heads 2, with
-  // fewer 3 (30 sequences up to 12829 keys, 6 heads on 3: 52 us at 3, 67 at 2), bf16 with up
+  // Blocks per SM (registers and shared memory allow no more): fp32 with up to 4 heads 3 (30
+  // sequences up to 12829 keys, 6 heads on 3: 52 us at 3, 67 at 2), with more 2; bf16 with up
   // to 8 heads 3, with 16 2.
-  static constexpr int kBlocks = (sizeof(T) == 2) == (H == 8) ? 3 : 2;
+  static constexpr int kBlocks = H <= (sizeof(T) == 2 ? 8 : 4) ? 3 : 2;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kSmem = kDecWarps * kRing;
   static constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
@@ -577,26 +577,28 @@ __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
 
 // fp32 on the CUDA cores, in packed pairs (two multiply-adds per instruction).
 // Scores: 8 lanes share a key (16 or 8 elements each, queries from shared memory,
-// two keys at a time), 4 keys side by side; 7 exchanges leave lane j of them with
-// head j (H = 2 or 4 heads: of them once or twice more). Outputs: a lane holds D / 32 elements of 8 heads. Weights pass through
-// shared memory, written twice as a pair so that they load as one. Outputs and
+// two keys at a time), 4 keys side by side; exchanges leave lane j of them with head
+// j % HF, HF the next power of two (heads from H on are zeros). Outputs: a lane holds
+// D / 32 elements of H heads. Weights pass through shared memory, written twice as a
+// pair so that they load as one. Outputs and
 // sums are kept in two levels (kFlush tiles, then all): one chain of 2400 keys
 // had twice the error. 24 sequences of 20000 to 30001 keys, 28 heads on 4: 390 us
-// (floor 384) while the clocks hold; back to back the power limit lowers them and
-// it takes 455 to 485.
+// (floor 384) while the clocks hold; one call after another the power limit lowers
+// them and it takes 420 to 433 (441 to 448 in runs of 8 with one head empty).
 template <int D, int H>
 struct DecFp32 {
   using S = DecShape<float, D, H>;
   static constexpr int E2 = D / 64, KK = S::kKeys, kFlush = 8;
+  static constexpr int HF = H <= 2 ? 2 : H <= 4 ? 4 : 8, HP = (H + 1) / 2 * 2;
   struct Shared {
     __align__(16) float q[H][D];
-    __align__(16) float2 p[kDecWarps][KK][H];
+    __align__(16) float2 p[kDecWarps][KK][HP];
   };
   const DecodeArgs& a;
   Shared& sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kg = lane >> 3, j = lane & 7;
   F2 o[H][E2], om[H][E2];
-  float m, l, lm;  // this lane's head: j % H
+  float m, l, lm;  // this lane's head: j % HF
   int n;
 
   __device__ __forceinline__ DecFp32(const DecodeArgs& a_, Shared& sh_) : a(a_), sh(sh_) {}
@@ -626,7 +628,7 @@ struct DecFp32 {
   }
 
   __device__ __forceinline__ void tile(const uint8_t* st, uint32_t here) {
-    float z[KK / 4];  // of key 4 g + kg and head j % H
+    float z[KK / 4];  // of key 4 g + kg and head j % HF
     float top = -INFINITY;
 #pragma unroll
     for (int g = 0; g < KK / 4; g += 2) {
@@ -650,7 +652,7 @@ struct DecFp32 {
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float d[H];
+        float d[HF] = {};
 #pragma unroll
         for (int h = 0; h < H; ++h) {
           const float2 v = unpack(acc[x][h]);
@@ -660,9 +662,9 @@ struct DecFp32 {
         // the half with that bit
 #pragma unroll
         for (int w = 4; w >= 1; w >>= 1) {
-          if (w >= H) {
+          if (w >= HF) {
 #pragma unroll
-            for (int k = 0; k < H; ++k) d[k] += __shfl_xor_sync(0xffffffffu, d[k], w);
+            for (int k = 0; k < HF; ++k) d[k] += __shfl_xor_sync(0xffffffffu, d[k], w);
           } else {
 #pragma unroll
             for (int k = 0; k < w; ++k) {
@@ -719,7 +721,7 @@ struct DecFp32 {
 #pragma unroll
         for (int e = 0; e < E2; ++e) {
           o[h][e] = fma2(pa, x[e], o[h][e]);
-          o[h + 1][e] = fma2(pb, x[e], o[h + 1][e]);
+          if (h + 1 < H) o[(h + 1) % H][e] = fma2(pb, x[e], o[(h + 1) % H][e]);
         }
       }
     }
@@ -1080,13 +1082,15 @@ namespace {
 struct DecLayout {
   size_t status, joins, part, total;
 };
-// Query heads of a run: those of a KV head in one run where its kernel can hold them
-// (bf16 16, fp32 8), in the smallest form that does: 144 bf16 sequences of 2987 keys, 12
-// heads of 64 on one KV head, 24 us in one run of 16 and 34 in two of 8; fp32, 4 sequences up
-// to 88849 keys with 4 heads on each of 2 KV heads, 92 us in a run of 4 and 108 in one of 8.
+// Query heads of a run: those of a KV head in as few runs as a kernel can hold (bf16 16, fp32
+// 8), the runs as even as they can be (100 fp32 sequences of 5000 keys, 12 heads on one KV
+// head: 168 us in two runs of 6, 188 in 8 and 4). 144 bf16 sequences of 2987 keys, 12 heads of 64 on one
+// KV head, 24 us in one run of 16 and 34 in two of 8; fp32, 4 sequences up to 88849 keys with 4
+// heads on each of 2 KV heads, 92 us in a run of 4 and 108 in one of 8 with empty heads.
 int dec_heads(int group, int dtype) {
   if (dtype == ADASPARK_BF16) return group <= 8 ? 8 : 16;
-  return group <= 2 ? 2 : group <= 4 ? 4 : 8;
+  const int runs = (group + 7) / 8;
+  return std::max(2, (group + runs - 1) / runs);
 }
 
 DecLayout dec_layout(int d, int heads) {
@@ -1154,6 +1158,12 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
                                   dim3(32 * S::H), 0, s, 1, a));
 }
 
+template <int H>
+int launch_fp32(const DecodeArgs& a, int d, int sms, cudaStream_t s) {
+  return d == 128 ? launch_decode<DecFp32<128, H>>(a, sms, s)
+                  : launch_decode<DecFp32<64, H>>(a, sms, s);
+}
+
 }  // namespace
 }  // namespace adaspark
 
@@ -1215,14 +1225,15 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
     return d == 128 ? launch_decode<DecBf16<128, 2>>(a, sms, s)
                     : launch_decode<DecBf16<64, 2>>(a, sms, s);
   }
-  if (heads == 2)
-    return d == 128 ? launch_decode<DecFp32<128, 2>>(a, sms, s)
-                    : launch_decode<DecFp32<64, 2>>(a, sms, s);
-  if (heads == 4)
-    return d == 128 ? launch_decode<DecFp32<128, 4>>(a, sms, s)
-                    : launch_decode<DecFp32<64, 4>>(a, sms, s);
-  return d == 128 ? launch_decode<DecFp32<128, 8>>(a, sms, s)
-                  : launch_decode<DecFp32<64, 8>>(a, sms, s);
+  switch (heads) {
+    case 2: return launch_fp32<2>(a, d, sms, s);
+    case 3: return launch_fp32<3>(a, d, sms, s);
+    case 4: return launch_fp32<4>(a, d, sms, s);
+    case 5: return launch_fp32<5>(a, d, sms, s);
+    case 6: return launch_fp32<6>(a, d, sms, s);
+    case 7: return launch_fp32<7>(a, d, sms, s);
+    default: return launch_fp32<8>(a, d, sms, s);
+  }
 }
 
 }  // extern "C"

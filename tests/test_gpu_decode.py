@@ -234,6 +234,15 @@ def test_strides_and_given_outputs():
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 6, 7, 10, 11, 17, 23])
+@pytest.mark.parametrize("spare_cols", [0, 3000])
+def test_every_group_size_in_fp32(group, d, spare_cols):
+    """Query heads per KV head, which fp32 cuts into runs of 2 to 8."""
+    x = _make([0, 1, 70, 333], 2 * group, 2, d, FP32, 16, spare_cols=spare_cols, seed=group)
+    _check(*x, *_run(*x))
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("lens,spare_cols", [([300, 0, 77], 0), ([300, 0, 4000], 3000),
                                              ([30] * 200, 0)])
