@@ -98,7 +98,7 @@ def build_calls(verbose: bool = False) -> str:
            "-I", os.path.join(troot, "include"),
            "-I", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
            "-I", os.path.join(cuda, "include"), src, "-o", CALLS, "-L", PKG, "-l:libadaspark.so",
-           "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
            "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -2,7 +2,7 @@
 // one step. These calls run once per layer and generated token, where the host
 // time of a call counts: through ctypes a decode call took 20 us on the host, 14
 // of them for checks, allocation and argument conversion; this way an append takes
-// 4.7 us on the host (3.1 with its output given), a decode call 5.6.
+// 4.1 us on the host (2.8 with its output given), a decode call as long as the GPU.
 //
 // Positional arguments only (the package's functions name and document them);
 // None stands for an output or a workspace to be allocated. Checks raise
@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -252,12 +253,13 @@ struct Rope {
   }
 };
 
+// Without the dispatcher, which would add 0.4 us to a call of 4.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device device) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  return at::Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 // Several dense tensors to be written. Small ones share one allocation, each on a
-// 256-byte boundary (an allocation costs a call 0.8 us); large ones have their
+// 256-byte boundary (an allocation costs a call 0.9 us); large ones have their
 // own, so that keeping one of them does not keep the others' memory.
 struct Piece {
   at::SmallVector<int64_t, 3> shape;
