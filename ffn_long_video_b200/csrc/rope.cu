@@ -725,9 +725,10 @@ __global__ void __launch_bounds__(128, kBwdBlocksPerSm<NORM>)
 // Sums the blocks' rows, 8 columns per block: column c of rows y, y + 128, ..., then
 // over y in halves. Latency-bound: 2.6 us for 444 rows of 256.
 __global__ void __launch_bounds__(1024)
-    rope_dw_kernel(const float* part, int rows, int d, float* dwq, float* dwk) {
+    rope_dw_kernel(WsHeader* hdr, const float* part, int rows, int d, float* dwq, float* dwk) {
   __shared__ float sum[128][9];
   dependency_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) hdr->status = hdr->detail = hdr->n_block_status = 0;
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int col = blockIdx.x * 8 + x;
   float acc = 0.f;
@@ -999,7 +1000,7 @@ int adaspark_kv_append(const void* K, int64_t k_ts, int64_t k_hs, const void* V,
 
 size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d, int dtype) {
   if (n_tokens < 0 || n_tokens > (1 << 30) || !head_sizes_ok(hq, hkv, d, dtype)) return 0;
-  return align_up((size_t)kBwdMaxParts * 2 * d * sizeof(float));
+  return align_up(sizeof(WsHeader)) + align_up((size_t)kBwdMaxParts * 2 * d * sizeof(float));
 }
 
 int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, const void* dK_out,
@@ -1021,7 +1022,9 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     const int rc = current_device(nullptr);
     if (rc != ADASPARK_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((w_q && cudaMemsetAsync(dw_q, 0, d * sizeof(float), s) != cudaSuccess) ||
+    if ((norm && workspace && aligned(workspace, kAlign) && workspace_bytes >= sizeof(WsHeader) &&
+         cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) ||
+        (w_q && cudaMemsetAsync(dw_q, 0, d * sizeof(float), s) != cudaSuccess) ||
         (w_k && cudaMemsetAsync(dw_k, 0, d * sizeof(float), s) != cudaSuccess))
       return ADASPARK_ECUDA;
     return ADASPARK_OK;
@@ -1048,7 +1051,9 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
   b.a.q = Q; b.a.k = K; b.a.qs = {q_ts, q_hs}; b.a.ks = {k_ts, k_hs};
   b.a.wq = w_q; b.a.wk = w_k; b.a.eps = eps; b.a.hq = hq; b.a.hkv = hkv;
   b.dq = dQ_out; b.dk = dK_out; b.dqs = {dq_ts, dq_hs}; b.dks = {dk_ts, dk_hs};
-  b.gq = dQ; b.gk = dK; b.part = static_cast<float*>(workspace);
+  b.gq = dQ; b.gk = dK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  b.part = norm ? reinterpret_cast<float*>(ws + align_up(sizeof(WsHeader))) : nullptr;
   int blocks = sms * kBwdBlocksPerSm<false>;
   if (norm)
     blocks = std::min(sms * kBwdBlocksPerSm<true>, kBwdMaxParts);
@@ -1066,8 +1071,9 @@ int adaspark_qk_rope_backward(const void* dQ_out, int64_t dq_ts, int64_t dq_hs, 
     e = dy_dtype == ADASPARK_BF16 ? dispatch_bwd<float, bf16>(b, d, il, s)
                                   : dispatch_bwd<float, float>(b, d, il, s);
   if (e == cudaSuccess && norm)
-    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 8), dim3(1024), 0, s, 1, b.part, blocks, d,
-               w_q ? dw_q : nullptr, w_k ? dw_k : nullptr);
+    e = launch_after("qk_rope_dw", rope_dw_kernel, dim3(2 * d / 8), dim3(1024), 0, s, 1,
+                     reinterpret_cast<WsHeader*>(ws), b.part, blocks, d, w_q ? dw_q : nullptr,
+                     w_k ? dw_k : nullptr);
   return cuda_status(e);
 }
 

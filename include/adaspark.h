@@ -582,7 +582,8 @@ size_t adaspark_qk_rope_backward_workspace(int n_tokens, int hq, int hkv, int d,
  *       written in full (not accumulated into); dw_q / dw_k needed and written
  *       where the weight is given. dQ may be dQ_out itself, dK dK_out (FP32, dense).
  *   workspace: as adaspark_qk_rope_backward_workspace says, 256-byte aligned;
- *       may be NULL without weights.
+ *       may be NULL without weights, where it is not touched. Its status word is
+ *       clear after the call (nothing in it can fail on the device).
  * Sums in fp32 in a fixed order (no atomics). n_tokens = 0 sets dw_q, dw_k to
  * zero. Errors as for adaspark_qk_rope. */
 int adaspark_qk_rope_backward(const void *dQ_out, int64_t dq_ts, int64_t dq_hs, const void *dK_out,

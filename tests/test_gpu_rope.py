@@ -426,3 +426,16 @@ def test_binding_refusals():
     q, _ = fb.qk_rope(Q[:1].expand(Q.shape[0], -1, -1), K, pos, freq, sections=kw["sections"])
     q2, _ = fb.qk_rope(Q[:1].repeat(Q.shape[0], 1, 1), K, pos, freq, sections=kw["sections"])
     assert torch.equal(q, q2)
+
+
+@pytest.mark.parametrize("n", [0, 1, 5000])
+def test_backward_workspace_has_a_clear_status(n):
+    g = torch.Generator().manual_seed(4)
+    Q, K = _rand(g, n, 4, 64, dtype=BF16), _rand(g, n, 2, 64, dtype=BF16)
+    w = torch.ones(64, dtype=BF16, device="cuda")
+    ws = torch.full((fb.qk_rope_backward_workspace_bytes(n, 4, 2, 64),), 255, dtype=torch.uint8,
+                    device="cuda")
+    freq = torch.from_numpy(fb.rope_frequencies(64)[0]).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    *_, ws2 = fb.qk_rope_backward(Q, K, pos, freq, Q, K, w_q=w, workspace=ws)
+    assert ws2.data_ptr() == ws.data_ptr() and fb.read_device_status(ws2) == (fb.OK, 0)
