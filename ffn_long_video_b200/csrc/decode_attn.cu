@@ -1084,9 +1084,10 @@ struct DecLayout {
 };
 // Query heads of a run: those of a KV head in as few runs as a kernel can hold (bf16 16, fp32
 // 8), the runs as even as they can be (100 fp32 sequences of 5000 keys, 12 heads on one KV
-// head: 168 us in two runs of 6, 188 in 8 and 4). 144 bf16 sequences of 2987 keys, 12 heads of 64 on one
-// KV head, 24 us in one run of 16 and 34 in two of 8; fp32, 4 sequences up to 88849 keys with 4
-// heads on each of 2 KV heads, 92 us in a run of 4 and 108 in one of 8 with empty heads.
+// head: 168 us in two runs of 6, 188 in 8 and 4). 144 bf16 sequences of 2987 keys, 12 heads of
+// 64 on one KV head, 24 us in one run of 16 and 34 in two of 8; fp32, 4 sequences up to 88849
+// keys with 4 heads on each of 2 KV heads, 92 us in a run of 4 and 108 in one of 8 with empty
+// heads.
 int dec_heads(int group, int dtype) {
   if (dtype == ADASPARK_BF16) return group <= 8 ? 8 : 16;
   const int runs = (group + 7) / 8;
@@ -1183,7 +1184,8 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
                          int hq, int hkv, int d, float scale, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, void* stream) {
   if (!Q || !block_table || !seq_lens || !out || !workspace) return ADASPARK_EINVAL;
-  if (n_seqs < 1 || n_seqs > kMaxSeqs || max_pages < 1 || !head_sizes_ok(hq, hkv, d, dtype)) return ADASPARK_EINVAL;
+  if (n_seqs < 1 || n_seqs > kMaxSeqs || max_pages < 1 || !head_sizes_ok(hq, hkv, d, dtype))
+    return ADASPARK_EINVAL;
   if (!std::isfinite(scale)) return ADASPARK_EINVAL;
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
   if (!cache_ok(k_cache, v_cache, cs, hkv, d, dtype)) return ADASPARK_EINVAL;

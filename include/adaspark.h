@@ -536,8 +536,9 @@ int adaspark_rope_frequencies(int rot, double base, int scaling, double factor, 
  *       bits; norms and rotation in fp32, one rounding to `dtype` at the end.
  *   w_q, w_k [d]: device, or NULL.
  *   Q_out, K_out: may be Q, K themselves with the same strides (in place).
- * n_tokens = 0 does nothing (arrays may then be NULL). Errors: ADASPARK_EINVAL for NULL pointers, bad
- * sizes, strides or alignment, eps < 0 or NaN, a magnitude that is not finite. */
+ * n_tokens = 0 does nothing (arrays may then be NULL). Errors: ADASPARK_EINVAL for
+ * NULL pointers, bad sizes, strides or alignment, eps < 0 or NaN, a magnitude that
+ * is not finite. */
 int adaspark_qk_rope(const void *Q, int64_t q_ts, int64_t q_hs, const void *K, int64_t k_ts,
                      int64_t k_hs, int dtype, const int32_t *positions, int n_axes,
                      const int32_t *sections, const double *freq, int rot, int interleaved,
@@ -622,9 +623,9 @@ size_t adaspark_kv_plan_workspace(int n_seqs);
  * a free count or a gift the pool cannot hold); a page number outside
  * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. A page
  * belongs to one sequence or to the list: one that two sequences hold would be
- * listed twice when both give it back. The arrays must not overlap. workspace: 256-byte aligned. ADASPARK_EINVAL for NULL
- * pointers, sizes < 1, n_seqs > 2^24, n_pages or n_rows > 2^30, a table_stride
- * below max_pages, a short workspace. */
+ * listed twice when both give it back. The arrays must not overlap. workspace:
+ * 256-byte aligned. ADASPARK_EINVAL for NULL pointers, sizes < 1, n_seqs > 2^24,
+ * n_pages or n_rows > 2^30, a table_stride below max_pages, a short workspace. */
 int adaspark_kv_plan(const int32_t *old_lens, const int32_t *new_lens, int n_seqs, int page_size,
                      int32_t *block_table, int64_t table_stride, int max_pages,
                      int32_t *free_pages, int n_pages, int32_t *n_free, int32_t *token_starts,
