@@ -804,11 +804,13 @@ cudaError_t launch_rope(const RopeArgs& a, bool il, int sms, cudaStream_t s) {
   constexpr int H = RopeMap<D, kRopeRun>::kHeads;
   const int64_t q_steps = (a.hq + H - 1) / H, k_steps = (a.hkv + H - 1) / H;
   const int64_t steps = q_steps + k_steps * (CACHE ? 2 : 1), n = a.n;
-  // A warp per step while that gives the longest-running warp less to do than walking whole
-  // tokens; a token's angles count as a step and a half.
+  // A warp per step for few tokens, warps that walk whole tokens for many, from a share of the
+  // resident warps that fits what was measured with norms (a warp per step, walking): bf16
+  // append of 28 + 4 heads, 1200 tokens 7.6 and 7.7 us, 1600 9.7 and 8.1; rope of 4 + 1 heads,
+  // 2400 tokens 4.0 and 4.1, 3600 5.5 and 4.8; fp32 rope of 28 + 4, 1200 tokens 10.6 and 11.0,
+  // 1600 12.9 and 12.8.
   const int64_t warps = (int64_t)sms * kRopeBlocks<T> * 4;
-  const bool walk =
-      ((n + warps - 1) / warps) * (steps + 1.5) < ((n * steps + warps - 1) / warps) * 2.5;
+  const bool walk = n > (sizeof(T) == 2 ? 0.22 + 0.65 / steps : 0.54) * warps;
   const char* name = CACHE ? "qk_rope_append" : "qk_rope";
   const dim3 block(128);
   if (walk) {
