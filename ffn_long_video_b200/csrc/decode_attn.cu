@@ -1127,10 +1127,13 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   a.tile_pages = S::kTile / a.cs.page_size;
   a.tile_rest = S::kTile % a.cs.page_size;
   // Few short runs: a cluster of blocks each, as many as the tables' longest run fills, with
-  // up to 4 tiles a block.
+  // up to 2 tiles a block, or 6 where the clusters have more blocks than the GPU SMs (bf16, 28
+  // heads on 4, pages of 16; cluster and line: 1 sequence of 1000 keys 6.2 and 6.9 us, of 2040
+  // 7.9 and 7.0; 12 of 3000 18.1 and 19.7, 12 of 1 to 3000 14.6 and 15.6; with 8 tiles a block 6
+  // of 1 to 4000 13.2 and 11.8).
   const int64_t run_tiles = dec_run_tiles(a.max_len, S::kTile);
   for (int C = kDecCluster; C >= 1; C /= 2) {
-    if (run_tiles * 2 <= C || run_tiles > 4 * C || runs * C > S::kBlocks * (int64_t)sms ||
+    if (run_tiles * 2 <= C || run_tiles > (runs * C > sms ? 6 : 2) * C || runs * C > S::kBlocks * (int64_t)sms ||
         runs * C > kDecMaxBlocks)
       continue;
     const int rc = allow_smem(decode_cluster_kernel<M>, S::kSmem);
@@ -1149,7 +1152,9 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
     rc = cuda_status(launch_after("decode_attn", decode_kernel<M>, dim3((unsigned)grid),
                                   dim3(kDecWarps * 32), smem, s, 1, a));
   if (rc != ADASPARK_OK) return rc;
-  // Parts per run, about: from some 16 on their loads go side by side in a block.
+  // Parts per run, about: from some 16 on their loads go side by side in a block (3 sequences of
+  // 12000 keys, 25 parts a run, 19.7 us and 20.8 with a warp for all parts of a head; 6 of 8000,
+  // 12 parts, 24.9 and 24.1).
   const unsigned entries = (unsigned)(a.by_run ? runs : grid);
   if (grid / runs >= 16)
     return cuda_status(launch_after("decode_join", decode_join_many_kernel<S>,
