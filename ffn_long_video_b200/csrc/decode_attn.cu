@@ -1133,8 +1133,8 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   // of 1 to 4000 13.2 and 11.8).
   const int64_t run_tiles = dec_run_tiles(a.max_len, S::kTile);
   for (int C = kDecCluster; C >= 1; C /= 2) {
-    if (run_tiles * 2 <= C || run_tiles > (runs * C > sms ? 6 : 2) * C || runs * C > S::kBlocks * (int64_t)sms ||
-        runs * C > kDecMaxBlocks)
+    if (run_tiles * 2 <= C || run_tiles > (runs * C > sms ? 6 : 2) * C ||
+        runs * C > S::kBlocks * (int64_t)sms || runs * C > kDecMaxBlocks)
       continue;
     const int rc = allow_smem(decode_cluster_kernel<M>, S::kSmem);
     if (rc != ADASPARK_OK) return rc;
