@@ -30,6 +30,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libadaspar
 OK, EINVAL, ECUDA, EUNSUPPORTED, EDEVICE = 0, -1, -2, -3, -4
 BF16, FP32 = 0, 1
 DEV_BAD_LAYOUT, DEV_TIMEOUT, DEV_RANGE, DEV_PAGES = 0x1, 0x2, 0x4, 0x8
+PLAN_REFUSED = 0x8100   # code (detail >> 8) of a page plan that was not carried out
 # AdaS-FFN token importance (ADASPARK_IMPORTANCE_*)
 IMPORTANCE_L2_SHARE, IMPORTANCE_L2SQ_SHARE, IMPORTANCE_SOFTMAX = 0, 1, 2
 # scaling of rotary frequencies (ADASPARK_ROPE_*)
@@ -660,7 +661,8 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_ro
     ``block_table`` int32 [n_seqs, max_pages], ``free_pages`` int32 [n_pages] and
     ``n_free`` int32 [1] in place; returns (slots [n_rows], positions [n_rows],
     token_starts [n_seqs + 1], workspace). read_device_status(workspace) tells
-    whether the plan was carried out."""
+    what went wrong: with detail >> 8 == PLAN_REFUSED nothing was carried out, else
+    all of it, with slot -1 where the pool has no such page."""
     if stream is not None:
         with _on(stream, old_lens, "old_lens"):
             return kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_rows,

@@ -183,7 +183,7 @@ __device__ __forceinline__ PlanTotals plan_sums(const PlanArgs& a, PlanShared* s
     a.starts[a.n_seqs] = ok ? t.rows : 0;
     if (COUNT && ok) *a.n_free = (int32_t)left;
     a.hdr->status = ok ? 0u : sound ? ADASPARK_DEV_PAGES : ADASPARK_DEV_BAD_LAYOUT;
-    a.hdr->detail = ok ? 0u : 0x8100u;
+    a.hdr->detail = ok ? 0u : ADASPARK_PLAN_REFUSED;
     a.hdr->n_block_status = a.blocks;
   }
   return t;
@@ -242,7 +242,8 @@ __device__ __forceinline__ void plan_row(const PlanArgs& a, int r, int pos, int 
 // Slots, positions, table and list entries, by `warps` warps of which this is
 // `warp`. A page that is taken is written to its table by whoever has its first
 // token, which is always a new one. Returns whether this thread met a page number
-// that the pool does not have.
+// that the pool does not have, for a new token or among the pages given back (which
+// go onto the list as they are, so that the plan can be undone).
 __device__ __forceinline__ bool plan_write(const PlanArgs& a, const PlanSums& p,
                                            const PlanTotals& t, int warp, int warps) {
   const int lane = threadIdx.x & 31, rows = t.ok ? t.rows : 0;
@@ -305,9 +306,11 @@ __device__ __forceinline__ bool plan_write(const PlanArgs& a, const PlanSums& p,
     }
   }
   if (!t.ok) return bad;
-  for (int g = t.take + warp * 32 + lane; g < t.give; g += warps * 32)
-    a.free_pages[t.n_free + t.give - 1 - g] =
-        plan_given(a, p, g, plan_find(p.give0, a.n_seqs, g));
+  for (int g = t.take + warp * 32 + lane; g < t.give; g += warps * 32) {
+    const int page = plan_given(a, p, g, plan_find(p.give0, a.n_seqs, g));
+    bad |= page < 0 || page >= a.n_pages;
+    a.free_pages[t.n_free + t.give - 1 - g] = page;
+  }
   return bad;
 }
 

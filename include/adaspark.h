@@ -65,6 +65,8 @@ typedef enum { ADASPARK_BF16 = 0, ADASPARK_FP32 = 1 } adaspark_dtype;
                                         /* fp16 range +-65504 (see adaspark_token_ffn)     */
 #define ADASPARK_DEV_PAGES        0x8u  /* adaspark_kv_plan: the free list holds too few    */
                                         /* pages for the new lengths                        */
+#define ADASPARK_PLAN_REFUSED     0x8100u /* code (detail bits 8-23) of a plan that was not */
+                                        /* carried out; others of BAD_LAYOUT were           */
 
 /* Human-readable name of a return code. Never NULL. */
 const char *adaspark_status_string(int status);
@@ -620,8 +622,11 @@ size_t adaspark_kv_plan_workspace(int n_seqs);
  * A plan that cannot be carried out changes nothing but its outputs (starts 0,
  * slots -1) and reports ADASPARK_DEV_PAGES (too few free pages) or
  * ADASPARK_DEV_BAD_LAYOUT (a length out of range, more than n_rows new tokens,
- * a free count or a gift the pool cannot hold); a page number outside
- * [0, n_pages) in a table or the list gives slot -1 and BAD_LAYOUT. A page
+ * a free count or a gift the pool cannot hold), with ADASPARK_PLAN_REFUSED as
+ * the code in the detail's bits 8-23. A page number outside [0, n_pages) that a
+ * new token needs, or that a sequence gives back, reports BAD_LAYOUT as well,
+ * but the plan is carried out (the code is another): the tokens get slot -1, a
+ * page given back goes onto the list as it is. A page
  * belongs to one sequence or to the list: one that two sequences hold would be
  * listed twice when both give it back. The arrays must not overlap. workspace:
  * 256-byte aligned. ADASPARK_EINVAL for NULL pointers, sizes < 1, n_seqs > 2^24,

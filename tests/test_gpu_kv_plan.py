@@ -198,3 +198,47 @@ def test_checks_of_plans_over_the_whole_gpu(n):
     *_, ws = fb.kv_plan(_t(more), _t(0 * more), st.d_table, st.d_free, st.d_n, page, 5000)
     assert fb.read_device_status(ws)[0] == fb.OK
     assert sorted(st.d_free.tolist()) == list(range(3 * cols + n)) and st.d_n.item() == 3 * cols + n
+
+
+@pytest.mark.parametrize("bad", [-1, 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("n,rows", [(2, 1), (2, 5000), (1500, 1), (1500, 60000)])
+def test_a_bad_page_given_back_is_flagged(n, rows, bad):
+    """One block, the whole GPU, and more sequences than a block sums: a page that the pool
+    does not have is flagged when its sequence ends or shrinks, in the plan that puts it on
+    the list, not only when another sequence takes it. The plan is carried out all the same,
+    which its detail tells from a refused one, and the plan back restores everything."""
+    st = State(n, 6, 4, 20)
+    lens = np.zeros(n, int)
+    lens[0], lens[n - 1] = 22, 9                   # 6 pages and 3
+    st.step(lens, max(rows, 31))
+    table, free, n_free = st.d_table.clone(), st.d_free.clone(), st.n_free
+    for new, at, col, give in ((0, 0, 2, 6), (11, 0, 5, 3), (0, n - 1, 0, 3)):
+        to = lens.copy()
+        to[at] = new
+        was = table[at, col].item()
+        st.d_table[at, col] = bad
+        *_, ws = fb.kv_plan(_t(lens), _t(to), st.d_table, st.d_free, st.d_n, 4, rows)
+        code, det = fb.read_device_status(ws)
+        listed = table[at].tolist()
+        listed[col] = bad
+        end = -(-int(lens[at]) // 4)
+        assert st.d_free[n_free:n_free + give].tolist() == listed[end - give:end][::-1]
+        assert st.d_n.item() == n_free + give
+        assert code == fb.EDEVICE and det & 0xff == fb.DEV_BAD_LAYOUT
+        assert det >> 8 != fb.PLAN_REFUSED
+        # back again: the bad page is taken, which is flagged, and the rest is as it was
+        slots, pos, _, ws = fb.kv_plan(_t(to), _t(lens), st.d_table, st.d_free, st.d_n, 4,
+                                       max(rows, 31))
+        code, det = fb.read_device_status(ws)
+        assert code == fb.EDEVICE and det & 0xff == fb.DEV_BAD_LAYOUT
+        assert det >> 8 != fb.PLAN_REFUSED
+        rows_back = int(lens[at]) - new
+        assert torch.equal(slots[:rows_back] == -1, pos[:rows_back] // 4 == col)
+        assert st.d_table[at, col].item() == bad and st.d_n.item() == n_free
+        st.d_table[at, col] = was
+        assert torch.equal(st.d_table, table) and torch.equal(st.d_free[:n_free], free[:n_free])
+        # a plan of the same lengths is clean; a refused one says so
+        *_, ws = fb.kv_plan(_t(lens), _t(lens), st.d_table, st.d_free, st.d_n, 4, rows)
+        assert fb.read_device_status(ws) == (fb.OK, 0)
+        *_, ws = fb.kv_plan(_t(lens), _t(lens * 0 - 1), st.d_table, st.d_free, st.d_n, 4, rows)
+        assert fb.read_device_status(ws)[1] >> 8 == fb.PLAN_REFUSED
