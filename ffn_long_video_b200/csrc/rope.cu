@@ -751,10 +751,9 @@ bool qk_rope_args_ok(const double* freq, int rot, int d, const int32_t* position
                      const int32_t* sections, float magnitude, const void* w_q, const void* w_k,
                      float eps) {
   if (!(eps >= 0.f) || !aligned(w_q, 16) || !aligned(w_k, 16)) return false;
-  if (rot < 0 || rot > d || rot % 16 != 0) return false;
-  if (rot == 0) return true;
+  if (rot < 0 || rot > d || rot % 16 != 0 || !std::isfinite(magnitude)) return false;
+  if (rot == 0) return true;  // positions, axes, sections and freq are not looked at
   if (!freq || !positions || !aligned(freq, 8) || !aligned(positions, 4)) return false;
-  if (!std::isfinite(magnitude)) return false;
   if (n_axes == 1) return true;
   if (n_axes != 3 || !sections) return false;
   int64_t sum = 0;
@@ -771,12 +770,13 @@ constexpr int kBwdMaxParts = 148 * kBwdBlocksPerSm<true>;  // blocks with sums f
 
 void set_rope(RopeArgs* a, const double* freq, int rot, const int32_t* positions, int n_axes,
               const int32_t* sections, float magnitude, int n) {
+  const bool axes = rot > 0 && n_axes == 3;
   a->freq = freq;
   a->rot = rot;
   a->pos = positions;
-  a->pos_axis = n_axes == 3 ? n : 0;
-  a->sec0 = n_axes == 3 ? sections[0] : rot / 2;
-  a->sec01 = n_axes == 3 ? sections[0] + sections[1] : rot / 2;
+  a->pos_axis = axes ? n : 0;
+  a->sec0 = axes ? sections[0] : rot / 2;
+  a->sec01 = axes ? sections[0] + sections[1] : rot / 2;
   a->magnitude = magnitude;
   a->n = n;
 }

@@ -534,8 +534,9 @@ int adaspark_rope_frequencies(int rot, double base, int scaling, double factor, 
  *       sums to rot/2: the first sections[0] pairs follow axis 0, the next
  *       sections[1] axis 1, the rest axis 2). Any int32 value.
  *   freq: device float64 [rot/2]; rot a multiple of 16, 0 <= rot <= d (0: no
- *       rotation, positions and freq may be NULL). Angles are reduced in 64
- *       bits; norms and rotation in fp32, one rounding to `dtype` at the end.
+ *       rotation; positions, n_axes, sections and freq are not looked at). Angles
+ *       are reduced in 64 bits; norms and rotation in fp32, one rounding to
+ *       `dtype` at the end.
  *   w_q, w_k [d]: device, or NULL.
  *   Q_out, K_out: may be Q, K themselves with the same strides (in place).
  * n_tokens = 0 does nothing (arrays may then be NULL). Errors: ADASPARK_EINVAL for

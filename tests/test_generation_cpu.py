@@ -216,6 +216,29 @@ def test_qk_rope_backward_refusals(change):
     assert _call("qk_rope_backward", order, base, change) == fb.EINVAL
 
 
+BWD_ORDER = ("gQ gq_ts gq_hs gK gk_ts gk_hs dy Q q_ts q_hs K k_ts k_hs dtype pos axes sec freq rot "
+             "il mag wq wk eps n hq hkv d dQ dK dwq dwk ws wsb stream")
+LAYER_ORDER = ("x Wq Wk Wv Wo Wg Wu Wd dtype ids off text C nv n hq hkv d D F pa pf pos axes sec "
+               "freq rot il mag wq wk eps y ws wsb stream")
+
+
+@pytest.mark.parametrize("mag", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("name", ["qk_rope", "qk_rope_append", "qk_rope_backward", "layer_rope"])
+def test_a_magnitude_that_is_not_finite_is_refused_without_a_rotation_too(name, mag):
+    base = dict(ROPE, rot=0, pos=None, freq=None, mag=mag, V=P, v_ts=256, v_hs=128, **CACHE)
+    if name == "qk_rope_backward":
+        base.update(gQ=P, gq_ts=1024, gq_hs=128, gK=P, gk_ts=256, gk_hs=128, dy=fb.FP32, dQ=P,
+                    dK=P, dwq=P, dwk=P, ws=P,
+                    wsb=fb.qk_rope_backward_workspace_bytes(7, 8, 2, 128, fb.BF16))
+    if name == "layer_rope":
+        base.update(x=P, Wq=P, Wk=P, Wv=P, Wo=P, Wg=P, Wu=P, Wd=P, ids=P, off=P, text=P, C=16,
+                    nv=512, n=544, hq=4, hkv=1, D=256, F=512, pa=0.7, pf=0.7, y=P, ws=P,
+                    wsb=fb.layer_workspace_bytes(544, 512, 16, 4, 1, 128, 256, 512))
+    order = dict(qk_rope=ROPE_ORDER, qk_rope_append=APPEND_ORDER, qk_rope_backward=BWD_ORDER,
+                 layer_rope=LAYER_ORDER)[name]
+    assert _call(name, order, base, {}) == fb.EINVAL
+
+
 PLAN_ORDER = "old new ns page table ts cols free pages nf starts slots pos rows ws wsb stream"
 
 

@@ -159,3 +159,26 @@ def test_layer_with_positions(rotate, norm):
         fb.layer(*args, freq=freq)
     with pytest.raises(fb.AdasparkError):
         fb.layer(*args, freq=freq, positions=pos, sections=(16, 24, 23))
+
+
+def test_layer_with_norms_looks_at_no_axes():
+    """The C call of a layer with norms and no rotation, three axes named and no sections:
+    the bits of the call with one axis."""
+    import ctypes
+    cfg = workloads.small_config(name="gen-norms", grid=(4, 8, 8), cube=(4, 4, 4), n_text=23, D=256,
+                                 hq=6, hkv=3, F=256, seed=74)
+    t = {k: v.cuda() for k, v in workloads.make_stack(cfg, 0).items()}
+    W = [t[k].t().contiguous() for k in ("W_q", "W_k", "W_v", "W_o")]
+    ids, off, text, _ = parity.layout_tensors(cfg, "cuda")
+    w = torch.linspace(0.5, 1.5, cfg.d).to(torch.bfloat16).cuda()
+    want, ws = fb.layer(t["x"], *W, t["W_gate"], t["W_up"], t["W_down"], ids, off, text, cfg.n_vis,
+                        cfg.hq, cfg.hkv, 0.7, 0.7, w_qnorm=w, w_knorm=w)
+    y = torch.zeros_like(want)
+    p = lambda x: ctypes.c_void_p(x.data_ptr())  # noqa: E731
+    args = [p(x) for x in (t["x"], *W, t["W_gate"], t["W_up"], t["W_down"])]
+    rc = fb.lib().adaspark_layer_rope(
+        *args, fb.BF16, p(ids), p(off), p(text), cfg.n_cubes, cfg.n_vis, cfg.n_tokens, cfg.hq,
+        cfg.hkv, cfg.d, cfg.D, cfg.F, 0.7, 0.7, None, 3, None, None, 0, 0, 1.0, p(w), p(w), 1e-6,
+        p(y), p(ws), ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == fb.OK and fb.read_device_status(ws)[0] == fb.OK
+    assert torch.equal(y, want)

@@ -439,3 +439,37 @@ def test_backward_workspace_has_a_clear_status(n):
     pos = torch.arange(n, dtype=torch.int32, device="cuda")
     *_, ws2 = fb.qk_rope_backward(Q, K, pos, freq, Q, K, w_q=w, workspace=ws)
     assert ws2.data_ptr() == ws.data_ptr() and fb.read_device_status(ws2) == (fb.OK, 0)
+
+
+@pytest.mark.parametrize("axes", [3, 0])
+def test_norms_alone_look_at_no_axes(axes):
+    """Without a rotation the C calls read neither positions nor sections, whatever
+    the number of axes: the bits of the calls with one axis."""
+    import ctypes
+    L, n, hq, hkv, d = fb.lib(), 50, 4, 2, 128
+    g = torch.Generator().manual_seed(6)
+    Q, K, V = (_rand(g, n, h, d, dtype=BF16) for h in (hq, hkv, hkv))
+    w = _rand(g, d, dtype=BF16)
+    want = fb.qk_rope(Q, K, None, None, w_q=w, w_k=w)
+    dQ, dK = _rand(g, n, hq, d), _rand(g, n, hkv, d)
+    want_g = fb.qk_rope_backward(dQ, dK, None, None, Q, K, w_q=w, w_k=w)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    rope = (None, axes, None, None, 0, 0, 1.0, p(w), p(w), 1e-6, n, hq, hkv, d)
+    qs, ks = (hq * d, d), (hkv * d, d)
+    q, k = torch.zeros_like(Q), torch.zeros_like(K)
+    assert L.adaspark_qk_rope(p(Q), *qs, p(K), *ks, fb.BF16, *rope, p(q), *qs, p(k), *ks,
+                              stream) == fb.OK
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    kc, vc = (torch.zeros(n, 1, hkv, d, dtype=BF16, device="cuda") for _ in range(2))
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    q.zero_()
+    assert L.adaspark_qk_rope_append(p(Q), *qs, p(K), *ks, p(V), *ks, fb.BF16, *rope, p(slots), p(kc),
+                                     p(vc), hkv * d, hkv * d, d, n, 1, p(q), *qs, stream) == fb.OK
+    assert torch.equal(q, want[0]) and torch.equal(kc[:, 0], want[1]) and torch.equal(vc[:, 0], V)
+    out = [torch.zeros_like(t) for t in want_g[:4]]
+    ws = want_g[4]
+    assert L.adaspark_qk_rope_backward(p(dQ), *qs, p(dK), *ks, fb.FP32, p(Q), *qs, p(K), *ks, fb.BF16,
+                                       *rope, *map(p, out), p(ws), ws.numel(), stream) == fb.OK
+    for a, b in zip(out, want_g):
+        assert torch.equal(a, b)
