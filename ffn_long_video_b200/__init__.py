@@ -464,8 +464,11 @@ def layer(x, W_q, W_k, W_v, W_o, W_gate, W_up, W_down, cube_ids, cube_offsets, t
     """A whole AdaSpark layer (projections, AdaS-Attn, output projection with the
     residual, AdaS-FFN); weights in [out, in] layout. Returns (y fp32, workspace).
     With ``freq`` (rotary positions) or ``w_qnorm`` / ``w_knorm`` (per-head norms)
-    queries and keys go through qk_rope before the attention."""
+    queries and keys go through qk_rope before the attention; ``positions`` or
+    ``sections`` without ``freq`` are refused."""
     import torch
+    if freq is None and (positions is not None or sections is not None):
+        raise ValueError("positions and sections need freq")
     for t, nm in ((x, "x"), (W_q, "W_q"), (W_k, "W_k"), (W_v, "W_v"), (W_o, "W_o"),
                   (W_gate, "W_gate"), (W_up, "W_up"), (W_down, "W_down"),
                   (cube_ids, "cube_ids"), (cube_offsets, "cube_offsets"),
@@ -598,8 +601,9 @@ def qk_rope(Q, K, positions, freq, w_q=None, w_k=None, eps=1e-6, interleaved=Fal
     """Per-head RMSNorm (with ``w_q`` / ``w_k``) and rotary positions of Q
     [N, hq, d] and K [N, hkv, d] (any token and head strides): returns the
     rotated (Q, K). ``freq`` float64 [rot/2] on the device (None: nothing is
-    rotated), ``positions`` int32 [N], or [3, N] with ``sections`` (pairs per
-    axis). ``out_q`` / ``out_k`` may be Q / K themselves."""
+    rotated, positions and sections are not looked at), ``positions`` int32 [N],
+    or [3, N] with ``sections`` (pairs per axis). ``out_q`` / ``out_k`` may be Q /
+    K themselves."""
     if stream is not None:
         with _on(stream, Q, "Q"):
             return qk_rope(Q, K, positions, freq, w_q, w_k, eps, interleaved, sections, magnitude,

@@ -309,3 +309,13 @@ def test_binding_refuses_host_tensors():
                  lambda: fb.decode_attn(x, c, c, torch.zeros(3, 2, dtype=torch.int32), i)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("given", [dict(positions=torch.zeros(4, dtype=torch.int32)),
+                                   dict(sections=(16, 24, 24)),
+                                   dict(positions=torch.zeros(4, dtype=torch.int32),
+                                        w_qnorm=torch.ones(128))])
+def test_layer_refuses_positions_without_frequencies(given):
+    """They would be dropped: the layer would run without its positions."""
+    with pytest.raises(ValueError, match="freq"):
+        fb.layer(*[torch.zeros(4, 4)] * 11, 2, 1, 1, 0.7, 0.7, **given)
