@@ -7,7 +7,9 @@ Every .cu / .cpp under csrc/ is compiled separately (in parallel) into _build/
 and linked into ffn_long_video_b200/libadaspark.so.  The CUDA runtime is linked
 statically; the driver API is reached through cudaGetDriverEntryPoint.
 binding/calls.cpp is compiled against the installed torch and linked to
-libadaspark.so beside it.
+libadaspark.so beside it. The library needs nvcc alone: where the binding cannot be
+built (no torch, no Python headers), that is said on stderr, and only its calls
+fail, when they are made.
 """
 from __future__ import annotations
 
@@ -74,22 +76,30 @@ def build(verbose: bool = False, ptxas_v: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    build_calls(verbose)
+    try:
+        build_calls(verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        print(f"{os.path.basename(CALLS)}, the binding of the generation calls, was not built: {e}",
+              file=sys.stderr)
     return LIB
 
 
 def build_calls(verbose: bool = False) -> str:
-    """_calls.so: the binding of the generation calls (needs libadaspark.so)."""
+    """_calls.so: the binding of the generation calls (needs libadaspark.so). Where it
+    has to be built and cannot be, none is left behind."""
     import sysconfig
 
     import torch
     src = os.path.join(PKG, "binding", "calls.cpp")
     troot = os.path.dirname(os.path.abspath(torch.__file__))
-    stamp = os.path.join(BUILD, "calls.torch")   # the torch it was compiled against
+    stamp = os.path.join(BUILD, "calls.torch")   # the torch and Python it was compiled against
+    now = f"{torch.__version__} {sys.implementation.cache_tag}"
     said = open(stamp).read() if os.path.exists(stamp) else ""
     newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "adaspark.h")))
-    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest and said == torch.__version__:
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest and said == now:
         return CALLS
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
     tlib = os.path.join(troot, "lib")
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
@@ -106,7 +116,7 @@ def build_calls(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"building _calls.so failed:\n{r.stdout}\n{r.stderr}")
     with open(stamp, "w") as f:
-        f.write(torch.__version__)
+        f.write(now)
     return CALLS
 
 
