@@ -1191,7 +1191,8 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   if (!Q || !block_table || !seq_lens || !out || !workspace) return ADASPARK_EINVAL;
   if (n_seqs < 1 || n_seqs > kMaxSeqs || max_pages < 1 || !head_sizes_ok(hq, hkv, d, dtype))
     return ADASPARK_EINVAL;
-  if (!std::isfinite(scale)) return ADASPARK_EINVAL;
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  if (!std::isfinite(scale_log2)) return ADASPARK_EINVAL;
   const CacheRows cs{c_ps, c_ts, c_hs, n_pages, page_size};
   if (!cache_ok(k_cache, v_cache, cs, hkv, d, dtype)) return ADASPARK_EINVAL;
   if ((int64_t)max_pages * page_size > INT32_MAX - 1024) return ADASPARK_EINVAL;
@@ -1217,7 +1218,7 @@ int adaspark_decode_attn(const void* Q, int64_t q_ts, int64_t q_hs, const void* 
   a.kc = k_cache; a.vc = v_cache; a.cs = cs;
   a.table = block_table; a.table_stride = table_stride; a.lens = seq_lens;
   a.out = out; a.lse = lse;
-  a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+  a.scale_log2 = scale_log2;
   a.n_seqs = n_seqs; a.max_len = max_pages * page_size;
   a.hq = hq; a.hkv = hkv; a.group = hq / hkv;
   a.hgroups = hgroups;

@@ -650,7 +650,7 @@ size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dt
  *   Q: device, [n_seqs] rows of hq heads; block_table: device int32, row i at
  *       i * table_stride, key j on page block_table[i][j / page_size];
  *   seq_lens [n_seqs]: device int32, 0 .. max_pages * page_size;
- *   scale: finite (1/sqrt(d) in adaspark_cube_attn);
+ *   scale: finite, and so is scale * log2(e) in float32 (1/sqrt(d) in adaspark_cube_attn);
  *   out [n_seqs, hq, d]: device, dense, may be Q itself; lse [n_seqs, hq]: device float32 or NULL;
  *   workspace: 256-byte aligned.
  * Nothing at or past a sequence's length is read (it may hold NaN). Values that

@@ -319,3 +319,13 @@ def test_layer_refuses_positions_without_frequencies(given):
     """They would be dropped: the layer would run without its positions."""
     with pytest.raises(ValueError, match="freq"):
         fb.layer(*[torch.zeros(4, 4)] * 11, 2, 1, 1, 0.7, 0.7, **given)
+
+
+@pytest.mark.parametrize("scale", [3.4e38, -2.4e38, float("inf"), float("nan")])
+def test_decode_refuses_a_scale_beyond_its_logarithm_base(scale):
+    """The scores are kept in base 2: a scale whose product with log2(e) overflows would make
+    a score of 0 NaN."""
+    base = dict(Q=P, q_ts=1024, q_hs=128, dtype=fb.BF16, table=P, ts=8, cols=8, lens=P, ns=5, hq=8,
+                hkv=2, d=128, scale=scale, out=P, lse=P, ws=P,
+                wsb=fb.decode_attn_workspace_bytes(5, 8, 2, 128, fb.BF16), stream=None, **CACHE)
+    assert _call("decode_attn", DECODE_ORDER, base, {}) == fb.EINVAL
