@@ -473,3 +473,37 @@ def test_norms_alone_look_at_no_axes(axes):
                                        *rope, *map(p, out), p(ws), ws.numel(), stream) == fb.OK
     for a, b in zip(out, want_g):
         assert torch.equal(a, b)
+
+
+# n beyond one walk of the warps (1776), so that some take a token more than others; the last
+# case takes 6 walks
+@pytest.mark.parametrize("n,hq,hkv,d,dtype", [(5001, 12, 2, 128, BF16), (4300, 5, 5, 128, BF16),
+                                              (2500, 7, 7, 64, FP32), (1777, 3, 1, 64, BF16),
+                                              (9000, 6, 1, 64, FP32)])
+def test_weight_gradients_count_every_row(n, hq, hkv, d, dtype):
+    """Heads of ones with signs have the inverse root 1, so without a rotation an element of
+    dw is a sum of n * heads signs, a whole number: a row that is lost, or counted twice, moves
+    it by 1.  r = rsqrt(1) may be off by 2 ulp (4 u), its product with x rounds 1 u; every sum
+    adds half a step: a lane's steps over its tokens, the lanes of a block at one element
+    (4 warps of 32 / (d/8) heads), the blocks' rows in 128 chains and 7 halvings. Below a half
+    all told."""
+    g = torch.Generator().manual_seed(n)
+    sign = lambda *s: (2.0 * torch.randint(0, 2, s, generator=g) - 1)  # noqa: E731
+    Q, K = sign(n, hq, d), sign(n, hkv, d)
+    dQ, dK = sign(n, hq, d), sign(n, hkv, d)
+    w = torch.ones(d, dtype=dtype, device="cuda")
+    dev = lambda t: t.to(dtype).cuda()  # noqa: E731
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    per = 256 // d                                   # heads of a warp's step
+    walks = -(-n // (4 * 3 * sms))
+    for rows in (slice(None), slice(n - 1, n), slice(n - 7, n - 3)):
+        mq, mk = torch.zeros_like(dQ), torch.zeros_like(dK)
+        mq[rows], mk[rows] = dQ[rows], dK[rows]
+        *_, dwq, dwk, _ = fb.qk_rope_backward(mq.cuda(), mk.cuda(), None, None, dev(Q), dev(K),
+                                              w_q=w, w_k=w, eps=0.0)
+        for got, x, dy, h in ((dwq, Q, mq, hq), (dwk, K, mk, hkv)):
+            want = (x.double() * dy.double()).sum((0, 1)).numpy()
+            depth = walks * -(-h // per) + 4 * per + -(-3 * sms // 128) + 7
+            bound = (5 + depth) * U * n * h
+            assert bound < 0.5
+            assert np.abs(_f64(got) - want).max() <= bound
