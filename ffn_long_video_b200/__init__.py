@@ -664,7 +664,9 @@ def kv_plan(old_lens, new_lens, block_table, free_pages, n_free, page_size, n_ro
     """One step's page plan on the device (adaspark_kv_plan): updates
     ``block_table`` int32 [n_seqs, max_pages], ``free_pages`` int32 [n_pages] and
     ``n_free`` int32 [1] in place; returns (slots [n_rows], positions [n_rows],
-    token_starts [n_seqs + 1], workspace). read_device_status(workspace) tells
+    token_starts [n_seqs + 1], workspace). ``positions`` count a sequence's tokens;
+    after a prompt rotated by three axes the rotary position of a text token lies a
+    constant of its sequence away. read_device_status(workspace) tells
     what went wrong: with detail >> 8 == PLAN_REFUSED nothing was carried out, else
     all of it, with slot -1 where the pool has no such page."""
     if stream is not None:

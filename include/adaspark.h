@@ -617,9 +617,12 @@ size_t adaspark_kv_plan_workspace(int n_seqs);
  *       list and count are as before.
  *   token_starts [n_seqs + 1]: out, rows of earlier sequences' new tokens, then
  *       the total;
- *   slots, positions [n_rows]: out, slot and position of every new token
- *       (sequences in order, positions ascending), -1 and 0 in rows past the
- *       total (as adaspark_qk_rope_append takes them).
+ *   slots, positions [n_rows]: out, slot (as adaspark_qk_rope_append takes it)
+ *       of every new token and its position in its sequence, counted in tokens
+ *       (sequences in order, positions ascending); -1 and 0 in rows past the
+ *       total. After a prompt that was rotated by time, height and width a text
+ *       token's rotary position is not this one but lies a constant of its
+ *       sequence away, which the caller adds.
  * A plan that cannot be carried out changes nothing but its outputs (starts 0,
  * slots -1) and reports ADASPARK_DEV_PAGES (too few free pages) or
  * ADASPARK_DEV_BAD_LAYOUT (a length out of range, more than n_rows new tokens,

@@ -182,3 +182,34 @@ def test_layer_with_norms_looks_at_no_axes():
         p(y), p(ws), ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
     assert rc == fb.OK and fb.read_device_status(ws)[0] == fb.OK
     assert torch.equal(y, want)
+
+
+def test_rotary_positions_after_a_video_lie_an_offset_from_the_plan():
+    """Tokens after a video prompt: the plan's positions count tokens; with the sequence's
+    offset, on one axis, they rotate as the prompt's three equal axes do, bit for bit."""
+    cfg = CASES["bf16"]
+    g = torch.Generator().manual_seed(5)
+    pos = torch.from_numpy(video_positions(cfg)).cuda()
+    d, sections = cfg.d, (cfg.d // 8, 3 * cfg.d // 16, 3 * cfg.d // 16)
+    freq = torch.from_numpy(fb.rope_frequencies(d, 1e6)[0]).cuda()
+    Q, K, V = (torch.randn(cfg.n_tokens, h, d, generator=g).to(torch.bfloat16).cuda()
+               for h in (cfg.hq, cfg.hkv, cfg.hkv))
+    want_q, want_k = fb.qk_rope(Q, K, pos, freq, sections=sections)
+    # two sequences: the video alone, and the video with five text tokens
+    at = [cfg.n_vis, cfg.n_vis + 5]
+    offset = torch.stack([pos[:, :n].max() + 1 - n for n in at]).to(torch.int32)
+    assert offset[0] == offset[1] < -32
+    lens, page = torch.tensor(at, dtype=torch.int32, device="cuda"), 16
+    cols = -(-cfg.n_tokens // page)
+    table = torch.full((2, cols), -1, dtype=torch.int32, device="cuda")
+    free = torch.arange(2 * cols, dtype=torch.int32, device="cuda")
+    n_free = torch.tensor([2 * cols], dtype=torch.int32, device="cuda")
+    fb.kv_plan(lens * 0, lens, table, free, n_free, page, sum(at))
+    slots, places, _, ws = fb.kv_plan(lens, lens + 1, table, free, n_free, page, 2)
+    assert fb.read_device_status(ws) == (fb.OK, 0) and places.tolist() == at
+    kc, vc = (torch.zeros(2 * cols, page, cfg.hkv, d, dtype=Q.dtype, device="cuda") for _ in range(2))
+    q = fb.qk_rope_append(Q[at], K[at], V[at], places + offset, freq, slots, kc, vc)
+    s = slots.long()
+    assert torch.equal(q, want_q[at]) and torch.equal(kc[s // page, s % page], want_k[at])
+    # the places themselves would not do
+    assert not torch.equal(fb.qk_rope(Q[at], K[at], places, freq)[0], want_q[at])
