@@ -302,7 +302,7 @@ __device__ __forceinline__ uint32_t dec_copy(const DecodeArgs& a, uint8_t* st, c
 
 // Ends a run, or the block's share of one: joins the warps' maxima, sums and
 // outputs and writes results or partial ones. The outputs pass through the stage
-// that each warp has just used (`used`; [8][D + 4] floats), the other stages are
+// that each warp has just used (`used`; [H][D + 4] floats), the other stages are
 // being filled for the tiles to come. All threads; ends with a barrier. `u`: tile
 // on the line where the block's share of the run began; `from`: that tile in the run.
 template <class M>
@@ -453,7 +453,8 @@ __device__ __forceinline__ void cluster_barrier() {
 // Few short runs: a cluster of blocks per run (no line to lay out), each with an
 // even share of its tiles; the parts are joined through the blocks' shared memory
 // and there is no second kernel (one sequence of 500 keys, 28 heads on 4, one call
-// after another: 5.2 us, 7.5 along the line). All branches around the barriers go
+// after another: 5.1 us; 6.5 along the line, under a table of 4113 pages of 16). All
+// branches around the barriers go
 // by the sequence's length, which the cluster shares.
 template <class M>
 __global__ void __launch_bounds__(kDecWarps * 32, M::S::kBlocks)
@@ -791,9 +792,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // 128 rows of a tcgen05 tile would hold 7 or 8 of them), and a lane's softmax
 // columns are its output columns. NT = 2: up to 16 heads, each load of a key feeds
 // two products. P goes to the second product as two bf16 parts (high and rest:
-// 2^-17 relative), which costs 8 more products per 16 keys and keeps the output as
-// near as fp32 weights would. 61 sequences up to 9001 keys, 16 heads on 2 of 128:
-// 53.8 us (floor 44.3); one of 65793, 28 on 4: 30.2 us with its join (floor 20.9).
+// 2^-17 relative), which costs 8 more products per 16 keys; with one, each weight
+// would be off by up to half a step of bf16. With two, 0.2 % of the outputs of the 61
+// sequences below round to a neighbour of the rounded exact value, 0.1 % with fp32
+// weights; the error against 64 bits is the rounding's, 1.671e-3, either way.
+// 61 sequences up to 9001 keys, 16 heads on 2 of 128: 54.4 us (floor 44.3); one of
+// 65793, 28 on 4: 30.6 us with its join (floor 20.9).
 template <int D, int NT>
 struct DecBf16 {
   using S = DecShape<__nv_bfloat16, D, 8 * NT>;
@@ -1117,8 +1121,8 @@ int launch_decode(DecodeArgs a, int sms, cudaStream_t s) {
   const int64_t tiles = runs * dec_run_tiles(a.max_len, S::kTile);
   // Blocks per SM: two, and three where the kernel allows it and blocks walk several runs
   // each: 256 bf16 sequences up to 300 keys, 28 heads on 4, 23 us at three and 25 at two; 61
-  // sequences up to 9001 keys, 16 heads on 2, 52 and 49 us. fp32 runs of 2 or 4 heads always
-  // three.
+  // sequences up to 9001 keys, 16 heads on 2, 52 and 49 us. fp32 runs of up to 4 heads
+  // always three.
   const int per_sm = sizeof(typename S::T) == 2 && runs <= sms ? 2 : S::kBlocks;
   int64_t grid = per_sm * (int64_t)sms;
   if (grid > kDecMaxBlocks) grid = kDecMaxBlocks;

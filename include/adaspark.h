@@ -661,8 +661,13 @@ size_t adaspark_decode_attn_workspace(int n_seqs, int hq, int hkv, int d, int dt
  * Results depend on the inputs, the sizes and max_pages alone (no atomics). A
  * length out of range counts as 0 and a page number outside [0, n_pages) as
  * absent keys; both report ADASPARK_DEV_BAD_LAYOUT. Errors: ADASPARK_EINVAL as
- * for the other calls, n_seqs or max_pages < 1, n_seqs > 2^24, or tables that could hold 2^31
- * tiles of 32 keys and 8 query heads, over all sequences and KV heads. */
+ * for the other calls, n_seqs or max_pages < 1, n_seqs > 2^24, max_pages * page_size
+ * > 2^31 - 1025, or tables that could hold 2^31 tiles over all sequences and KV heads
+ * (a tile is 64 keys in bf16, 32 in fp32, twice as many at d = 64, of up to 16 query
+ * heads of a KV head in bf16, 8 in fp32). Outputs are divided after the sum: values
+ * near the end of float32's range may overflow in it. The form of the kernel follows
+ * max_pages, not the lengths: a narrower view of the table (max_pages below
+ * table_stride) selects the faster one for short sequences. */
 int adaspark_decode_attn(const void *Q, int64_t q_ts, int64_t q_hs, const void *k_cache,
                          const void *v_cache, int64_t c_ps, int64_t c_ts, int64_t c_hs,
                          int n_pages, int page_size, int dtype, const int32_t *block_table,
